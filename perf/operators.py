@@ -1,0 +1,401 @@
+"""The gated linear recurrence and the norms around a mixer block: cases, plain forms and exact values.
+
+Plain forms (`own = False`) are elementary torch operations in 32 bits, rounded once at the end; the recurrence is
+a doubling scan over the tokens.  With `own = True`, `run` makes the library's calls.
+
+    a = exp(-softplus(A_P)), g = sigmoid(I_P), u = beta g x with beta = 1, 1 - a or sqrt(1 - a^2)
+    gated scan    h_t = a_t h_{t-1} + u_t, y = h                          [B,H,N,d_h]
+    norm in       r' = r + s p, u = w r' / sqrt(mean r'^2 + eps)          [rows,E]
+    norm out      t = y silu(z), o = w t / sqrt(mean t^2 + eps)           [B,H,N,d_h] -> [B,N,H d_h]
+                  (gate first; norm first: o = w silu(z) y / sqrt(mean y^2 + eps))
+"""
+import math
+
+import torch
+
+own = False
+
+EPS = 1e-5
+SCALES = ("plain", "convex", "unit")  # beta = 1, 1 - a, sqrt(1 - a^2)
+
+
+def listed():
+    return [
+        # one interactive sequence of a small model: the shortest call there is
+        dict(name="step 1x2x32 f32", op="step", S=1, H=2, d=32, dtype="f32", scale="convex", gate=False),
+        # a serving batch, one token for each of 256 sequences
+        dict(name="step 256x32x64 bf16", op="step", S=256, H=32, d=64, dtype="bf16", scale="unit", gate=True),
+        # a short ragged prompt in full precision
+        dict(name="scan 1x2x257x32 f32", op="scan", B=1, H=2, N=257, d=32, dtype="f32", scale="plain", gate=True,
+             packed=False, init=False),
+        # a training batch
+        dict(name="scan 4x16x2048x64 bf16", op="scan", B=4, H=16, N=2048, d=64, dtype="bf16", scale="unit", gate=True,
+             packed=False, init=False),
+        # a long document, continued from an earlier segment's state: the largest
+        dict(name="scan 1x16x65536x64 bf16", op="scan", B=1, H=16, N=65536, d=64, dtype="bf16", scale="unit",
+             gate=True, packed=False, init=True),
+        # the training batch's backward, documents packed into one row (a decay of zero at each start)
+        dict(name="scan back 4x16x2048x64 bf16", op="scan_back", B=4, H=16, N=2048, d=64, dtype="bf16", scale="unit",
+             gate=True, packed=True, init=False),
+        # a ragged length in full precision, the state carried in and out
+        dict(name="scan back 2x16x4095x64 f32", op="scan_back", B=2, H=16, N=4095, d=64, dtype="f32", scale="convex",
+             gate=False, packed=False, init=True),
+        # the serving batch's residual stream
+        dict(name="norm in 256x2048 bf16", op="norm_in", rows=256, E=2048, dtype="bf16", scaled=True),
+        # the training batch's residual stream, backward
+        dict(name="norm in back 8192x1024 bf16", op="norm_in_back", rows=8192, E=1024, dtype="bf16", scaled=True),
+        # a serving batch's mixer output, one token a sequence, each head normalised for itself
+        dict(name="norm out 256x32x1x64 bf16", op="norm_out", B=256, H=32, N=1, d=64, dtype="bf16", groups=32,
+             gate_first=False),
+        # a training batch's mixer output
+        dict(name="norm out 2x16x4096x64 bf16", op="norm_out", B=2, H=16, N=4096, d=64, dtype="bf16", groups=1,
+             gate_first=True),
+        # and its backward
+        dict(name="norm out back 4x16x2048x64 bf16", op="norm_out_back", B=4, H=16, N=2048, d=64, dtype="bf16",
+             groups=1, gate_first=True),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(("step", "scan", "scan", "scan_back", "scan_back", "norm_in", "norm_in_back", "norm_out",
+                     "norm_out_back"))
+    dtype = rng.choice(("bf16", "bf16", "f32"))
+    most = 16 << 20  # elements: below the largest listed case's bytes in every operator and type
+    if op == "step":
+        return dict(op=op, S=_log_int(rng, 1, 1024), H=_log_int(rng, 1, 64), d=rng.choice((32, 64, 64, 33, 128)),
+                    dtype=dtype, scale=rng.choice(SCALES), gate=rng.random() < 0.5)
+    if op in ("scan", "scan_back"):
+        d, H = rng.choice((32, 64, 64, 64, 33, 128)), _log_int(rng, 1, 32)
+        N = _log_int(rng, 1, min(65536, most // (d * H)))
+        B = _log_int(rng, 1, max(1, min(16, most // (d * H * N))))
+        return dict(op=op, B=B, H=H, N=N, d=d, dtype=dtype, scale=rng.choice(SCALES), gate=rng.random() < 0.5,
+                    packed=rng.random() < 0.3, init=rng.random() < 0.5)
+    if op in ("norm_in", "norm_in_back"):
+        E = rng.choice((64, 512, 1000, 1024, 1025, 2048, 2560, 4096, 8192))
+        return dict(op=op, rows=_log_int(rng, 1, most // E), E=E, dtype=dtype, scaled=rng.random() < 0.7)
+    d, H = rng.choice((32, 64, 64, 64, 33, 128)), rng.choice((1, 2, 8, 12, 16, 20, 32, 64))
+    N = _log_int(rng, 1, min(65536, most // (d * H)))
+    B = _log_int(rng, 1, max(1, min(64, most // (d * H * N))))
+    return dict(op=op, B=B, H=H, N=N, d=d, dtype=dtype, groups=rng.choice((1, 1, H)), gate_first=rng.random() < 0.6)
+
+
+def _elements(c):
+    if c["op"] == "step":
+        return c["S"] * c["H"] * c["d"]
+    if "rows" in c:
+        return c["rows"] * c["E"]
+    return c["B"] * c["H"] * c["N"] * c["d"]
+
+
+def work(case):
+    c, n = case, _elements(case)
+    s = 2 if c["dtype"] == "bf16" else 4
+    op = c["op"]
+    if op == "step":  # x, A_P (I_P) read, the state read and written
+        return {"bytes": n * ((3 if c["gate"] else 2) * s + 8), "flops": 16 * n}
+    if op == "scan":  # x, A_P (I_P) read, y written, the states in and out
+        return {"bytes": n * ((3 if c["gate"] else 2) * s + 4) + (2 if c["init"] else 1) * 4 * n // c["N"],
+                "flops": 16 * n}
+    if op == "scan_back":  # x, A_P (I_P), y, dy read, their gradients written
+        k = 3 if c["gate"] else 2
+        return {"bytes": n * (k * s + 8 + 4 * k) + (12 if c["init"] else 0) * n // c["N"], "flops": 40 * n}
+    if op == "norm_in":  # r, p read, r', u written
+        return {"bytes": n * (8 + 2 * s) + 8 * c["E"], "flops": 7 * n}
+    if op == "norm_in_back":  # du, dr', r', p read, dr, dp written
+        return {"bytes": n * (2 * s + 16) + 16 * c["E"], "flops": 16 * n}
+    if op == "norm_out":  # y, z read, o written
+        return {"bytes": n * (4 + 2 * s) + 4 * c["H"] * c["d"], "flops": 12 * n}
+    return {"bytes": n * (12 + 2 * s) + 8 * c["H"] * c["d"], "flops": 30 * n}  # y, z, do read, dy, dz written
+
+
+def prepare(case, seed):
+    c = dict(case)
+    dev = "cuda" if torch.cuda.is_available() else "cpu"
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(seed)
+    dt = torch.bfloat16 if c["dtype"] == "bf16" else torch.float32
+
+    def normal(*shape):
+        return torch.randn(shape, generator=gen, device=dev)
+
+    def silu(v):
+        return v / (1 + torch.exp(-v))
+
+    st = {"c": c}
+    op = c["op"]
+    if op in ("step", "scan", "scan_back"):
+        shape = (c["S"], c["H"], c["d"]) if op == "step" else (c["B"], c["H"], c["N"], c["d"])
+        st["x"] = silu(normal(*shape)).to(dt)
+        A = normal(*shape) - 3
+        if c.get("packed"):  # a new document starts here: an infinite logit, so a = 0
+            A[:, :, torch.rand(c["N"], generator=gen, device=dev) < 1 / 256, :] = math.inf
+        st["A"] = A.to(dt)
+        st["I"] = normal(*shape).to(dt) if c["gate"] else None
+        state = (c["B"], c["H"], c["d"]) if op != "step" else shape
+        if op == "step":
+            st["state0"] = normal(*shape)
+            st["state"] = torch.empty_like(st["state0"])
+        else:
+            st["h0"] = normal(*state) if c["init"] else None
+        if op == "scan_back":
+            st["y"] = _scan_plain(st["x"], st["A"], st["I"], st["h0"], c["scale"])
+            st["dy"] = normal(*shape)
+            st["dlast"] = normal(*state) if c["init"] else None
+    elif op in ("norm_in", "norm_in_back"):
+        R, E = c["rows"], c["E"]
+        st["p"] = normal(R, E).to(dt)
+        st["s"] = 0.1 + 0.05 * normal(E) if c["scaled"] else None
+        st["w"] = 1 + 0.1 * normal(E)
+        st["r"] = 2 * normal(R, E)  # the residual stream: r, in the backward pass r'
+        if op == "norm_in_back":
+            st["du"], st["dr"] = normal(R, E).to(dt), normal(R, E)
+    else:
+        B, H, N, d = c["B"], c["H"], c["N"], c["d"]
+        st["y"] = normal(B, H, N, d)
+        st["z"] = normal(B, N, H * d).to(dt)
+        st["w"] = 1 + 0.1 * normal(H * d)
+        if op == "norm_out_back":
+            st["do"] = normal(B, N, H * d).to(dt)
+    return st
+
+
+# ---- the plain forms ----
+
+
+def _gates(A, I, scale):
+    A = A.float()
+    a, rest = 1 / (1 + torch.exp(A)), 1 / (1 + torch.exp(-A))  # a and 1 - a
+    beta = {"plain": torch.ones_like(a), "convex": rest, "unit": torch.sqrt(rest * (1 + a))}[scale]
+    g = 1 / (1 + torch.exp(-I.float())) if I is not None else torch.ones_like(a)
+    return a, rest, beta, g
+
+
+def _scan(a, u):
+    """h_t = a_t h_{t-1} + u_t along dimension -2 from zero, by doubling the reach of every token."""
+    n, reach = a.shape[-2], 1
+    while reach < n:
+        u = torch.cat((u[..., :reach, :], u[..., reach:, :] + a[..., reach:, :] * u[..., :-reach, :]), -2)
+        a = torch.cat((a[..., :reach, :], a[..., reach:, :] * a[..., :-reach, :]), -2)
+        reach *= 2
+    return u
+
+
+def _scan_plain(x, A, I, h0, scale):
+    a, _, beta, g = _gates(A, I, scale)
+    u = beta * g * x.float()
+    if h0 is not None:
+        u[..., 0, :] += a[..., 0, :] * h0
+    return _scan(a, u)
+
+
+def _scan_back_plain(x, A, I, h0, y, dy, dlast, scale):
+    a, rest, beta, g = _gates(A, I, scale)
+    x = x.float()
+    after = torch.cat((a[..., 1:, :], torch.zeros_like(a[..., :1, :])), -2)  # a_{t+1}
+    lam = dy.clone()
+    if dlast is not None:
+        lam[..., -1, :] += dlast
+    lam = _scan(after.flip(-2), lam.flip(-2)).flip(-2)
+    before = torch.cat(((h0 if h0 is not None else torch.zeros_like(y[..., 0, :])).unsqueeze(-2), y[..., :-1, :]), -2)
+    dbeta = {"plain": torch.zeros_like(a), "convex": a * rest, "unit": a * a * torch.sqrt(rest / (1 + a))}[scale]
+    out = {"dx": lam * beta * g, "dA": lam * (dbeta * g * x - a * rest * before)}
+    if I is not None:
+        out["dI"] = lam * beta * x * g * (1 - g)
+    if h0 is not None:
+        out["dh0"] = a[..., 0, :] * lam[..., 0, :]
+    return out
+
+
+def _norm_in_plain(r, p, s, w, dt):
+    r2 = r + (p.float() if s is None else s * p.float())
+    u = r2 * (torch.mean(r2 * r2, -1, keepdim=True) + EPS).rsqrt() * w
+    return {"r": r2, "u": u.to(dt)}
+
+
+def _norm_in_back_plain(du, dr, r, p, s, w):
+    du, p = du.float(), p.float()
+    k = (torch.mean(r * r, -1, keepdim=True) + EPS).rsqrt()
+    c = du * w
+    d = dr + k * c - k ** 3 * torch.mean(c * r, -1, keepdim=True) * r
+    out = {"dr": d, "dp": d if s is None else d * s, "dw": (du * r * k).sum(0)}
+    if s is not None:
+        out["ds"] = (d * p).sum(0)
+    return out
+
+
+def _norm_out_plain(y, z, w, groups, gate_first, dt):
+    B, H, N, d = y.shape
+    y = y.transpose(1, 2).reshape(B, N, groups, H * d // groups)
+    z = z.float().view(y.shape)
+    gate = z / (1 + torch.exp(-z))
+    t = y * gate if gate_first else y
+    n = t * (torch.mean(t * t, -1, keepdim=True) + EPS).rsqrt()
+    o = n * w.view(groups, -1) if gate_first else n * w.view(groups, -1) * gate
+    return o.view(B, N, H * d).to(dt)
+
+
+def _norm_out_back_plain(do, y, z, w, groups, gate_first):
+    B, H, N, d = y.shape
+    y = y.transpose(1, 2).reshape(B, N, groups, H * d // groups)
+    z, do, w = z.float().view(y.shape), do.float().view(y.shape), w.view(groups, -1)
+    sig = 1 / (1 + torch.exp(-z))
+    gate, slope = z * sig, sig * (1 + z * (1 - sig))
+    t = y * gate if gate_first else y
+    k = (torch.mean(t * t, -1, keepdim=True) + EPS).rsqrt()
+    c = do * w if gate_first else do * w * gate
+    dt = k * c - k ** 3 * torch.mean(c * t, -1, keepdim=True) * t
+    if gate_first:
+        dy, dz, dw = dt * gate, dt * y * slope, (do * t * k).sum((0, 1))
+    else:
+        dy, dz, dw = dt, do * w * y * k * slope, (do * y * k * gate).sum((0, 1))
+    return {"dy": dy.view(B, N, H, d).transpose(1, 2).contiguous(), "dz": dz.view(B, N, H * d), "dw": dw.view(-1)}
+
+
+def run(state):
+    st, c = state, state["c"]
+    op = c["op"]
+    if own:
+        return _run_own(st, c)
+    dt = torch.bfloat16 if c["dtype"] == "bf16" else torch.float32
+    if op == "step":
+        a, _, beta, g = _gates(st["A"], st["I"], c["scale"])
+        return a * st["state0"] + beta * g * st["x"].float()
+    if op == "scan":
+        y = _scan_plain(st["x"], st["A"], st["I"], st["h0"], c["scale"])
+        return {"y": y, "last": y[..., -1, :].contiguous()}
+    if op == "scan_back":
+        return _scan_back_plain(st["x"], st["A"], st["I"], st["h0"], st["y"], st["dy"], st["dlast"], c["scale"])
+    if op == "norm_in":
+        return _norm_in_plain(st["r"], st["p"], st["s"], st["w"], dt)
+    if op == "norm_in_back":
+        return _norm_in_back_plain(st["du"], st["dr"], st["r"], st["p"], st["s"], st["w"])
+    if op == "norm_out":
+        return _norm_out_plain(st["y"], st["z"], st["w"], c["groups"], c["gate_first"], dt)
+    return _norm_out_back_plain(st["do"], st["y"], st["z"], st["w"], c["groups"], c["gate_first"])
+
+
+def _run_own(st, c):
+    from mamba_ssd_sequence_amd import ssd
+
+    op = c["op"]
+    if op == "step":
+        # the states before the step stay as they are, so that a pass can be repeated
+        return ssd.gated_scan_step(st["x"], st["A"], st["I"], st["state0"], scale=SCALES.index(c["scale"]),
+                                   new_state=st["state"])
+    if op == "scan":
+        x = st["x"]
+        last = torch.empty((c["B"], c["H"], c["d"]), dtype=torch.float32, device=x.device)
+        y = ssd.gated_scan(x, st["A"], st["I"], scale=SCALES.index(c["scale"]), initial_state=st["h0"],
+                           final_state=last)
+        return {"y": y, "last": last}
+    if op == "scan_back":
+        dx, dA, dI, dh0 = ssd.gated_scan_backward(st["x"], st["A"], st["I"], st["y"], st["dy"],
+                                                  scale=SCALES.index(c["scale"]), initial_state=st["h0"],
+                                                  d_final_state=st["dlast"])
+        out = {"dx": dx, "dA": dA}
+        if dI is not None:
+            out["dI"] = dI
+        if dh0 is not None:
+            out["dh0"] = dh0
+        return out
+    if op == "norm_in":
+        r, u = ssd.norm_in(st["r"], st["p"], st["s"], st["w"], EPS)
+        return {"r": r, "u": u}
+    if op == "norm_in_back":
+        dr, dp, dw, ds = ssd.norm_in_backward(st["du"], st["dr"], st["r"], st["p"], st["s"], st["w"], EPS)
+        out = {"dr": dr, "dp": dp, "dw": dw}
+        if ds is not None:
+            out["ds"] = ds
+        return out
+    if op == "norm_out":
+        return ssd.norm_out(st["y"], st["z"], st["w"], EPS, groups=c["groups"], gate_first=c["gate_first"])
+    dy, dz, dw = ssd.norm_out_backward(st["do"], st["y"], st["z"], st["w"], EPS, groups=c["groups"],
+                                       gate_first=c["gate_first"])
+    return {"dy": dy, "dz": dz, "dw": dw}
+
+
+# ---- the definitions in 64 bits, a token after the other ----
+
+
+def _exact_gates(A, I, scale):
+    A = A.double()
+    a, rest = torch.sigmoid(-A), torch.sigmoid(A)
+    g = torch.sigmoid(I.double()) if I is not None else torch.ones_like(A)
+    if scale == "plain":
+        return a, rest, torch.ones_like(a), torch.zeros_like(a), g
+    if scale == "convex":
+        return a, rest, rest, a * rest, g  # d(1 - a)/dA_P = a (1 - a)
+    beta = torch.sqrt(rest * (1 + a))
+    return a, rest, beta, torch.where(beta > 0, a * a * rest / beta, 0.0), g  # -(a / beta) da/dA_P
+
+
+def exact(case, seed):
+    st, c = prepare(case, seed), case
+    op = c["op"]
+    if op in ("step", "scan", "scan_back"):
+        a, rest, beta, dbeta, g = _exact_gates(st["A"], st["I"], c["scale"])
+        x = st["x"].double()
+        u = beta * g * x
+        if op == "step":
+            return st["state0"].double() * a + u
+        h0 = st["h0"].double() if st["h0"] is not None else torch.zeros_like(u[:, :, 0])
+        if op == "scan":
+            h = h0
+            for t in range(c["N"]):
+                h = torch.addcmul(u[:, :, t], a[:, :, t], h)
+                u[:, :, t] = h
+            return {"y": u, "last": h}
+        lam = st["dy"].double()
+        if st["dlast"] is not None:
+            lam[:, :, -1] += st["dlast"].double()
+        for t in range(c["N"] - 2, -1, -1):
+            lam[:, :, t] += a[:, :, t + 1] * lam[:, :, t + 1]
+        prev = torch.empty_like(lam)
+        prev[:, :, 0] = h0
+        prev[:, :, 1:] = st["y"].double()[:, :, :-1]
+        out = {"dx": lam * beta * g, "dA": lam * dbeta * g * x - lam * prev * a * rest}
+        if st["I"] is not None:
+            out["dI"] = lam * beta * x * g * torch.sigmoid(-st["I"].double())
+        if st["h0"] is not None:
+            out["dh0"] = lam[:, :, 0] * a[:, :, 0]
+        return out
+    w = st["w"].double()
+    if op in ("norm_in", "norm_in_back"):
+        p, r = st["p"].double(), st["r"].double()
+        s = st["s"].double() if st["s"] is not None else torch.ones_like(w)
+        if op == "norm_in":
+            r = r + s * p
+            return {"r": r, "u": w * r / torch.sqrt(r.square().mean(1, keepdim=True) + EPS)}
+        var = r.square().mean(1, keepdim=True) + EPS
+        hat = r / var.sqrt()
+        c1 = st["du"].double() * w
+        d = st["dr"].double() + (c1 - hat * (c1 * hat).mean(1, keepdim=True)) / var.sqrt()
+        out = {"dr": d, "dp": s * d, "dw": (st["du"].double() * hat).sum(0)}
+        if st["s"] is not None:
+            out["ds"] = (d * p).sum(0)
+        return out
+    B, H, N, d = st["y"].shape
+    G = c["groups"]
+    y = st["y"].double().permute(0, 2, 1, 3).reshape(B * N, G, -1)
+    z = st["z"].double().reshape(y.shape)
+    w = w.reshape(1, G, -1)
+    gate = z * torch.sigmoid(z)
+    t = gate * y if c["gate_first"] else y
+    root = torch.sqrt(t.square().mean(2, keepdim=True) + EPS)
+    after = 1.0 if c["gate_first"] else gate
+    if op == "norm_out":
+        return (t / root * w * after).reshape(B, N, H * d)
+    do = st["do"].double().reshape(y.shape)
+    slope = torch.sigmoid(z) + gate * torch.sigmoid(-z)
+    c1, hat = do * w * after, t / root
+    dt = (c1 - hat * (c1 * hat).mean(2, keepdim=True)) / root
+    if c["gate_first"]:
+        dy, dz = dt * gate, dt * y * slope
+    else:
+        dy, dz = dt, do * w * hat * slope
+    dw = (do * hat * after).sum(0).reshape(-1)
+    return {"dy": dy.reshape(B, N, H, d).permute(0, 2, 1, 3).contiguous(), "dz": dz.reshape(B, N, H * d), "dw": dw}

@@ -388,6 +388,181 @@ ssd_status ssd_prep_amask_backward(const float* A_proj, const float* dt_proj, co
                                    const float* ddt, int64_t B, int64_t H, int64_t N,
                                    float* d_A_proj, float* d_dt_proj, hipStream_t stream);
 
+/*
+ * The gated linear recurrence -- the A-mask of Algorithms 4 and 5 with a decay
+ * for every channel instead of one for a whole head, and a state of one value
+ * a channel:
+ *
+ *     a_t = exp(-softplus(A_P,t)) = 1 / (1 + e^{A_P,t}),   g_t = sigmoid(I_P,t)
+ *     h_t = a_t h_{t-1} + beta_t g_t x_t,                  y_t = h_t
+ *
+ * with beta from ssd_input_scale.  It is a sequence mixer of the same arrays
+ * as ssd_forward: [B,H,N,d_h] in, y [B,H,N,d_h] f32 out, states handed from
+ * segment to segment and to single-token steps.  Not on the pages.
+ *
+ * A_P = +inf gives a = 0 exactly: nothing from before the token is kept, which
+ * starts a new sequence inside a row (gradients included).  A_P = -inf gives
+ * a = 1 and beta = 0 (SSD_INPUT_PLAIN: 1): the state is kept.  A NaN or an
+ * infinite x reaches the outputs of its channel from its token on, up to the
+ * next such start or beyond it (0 inf = NaN, as in the recurrence itself).
+ *
+ * SSD_INPUT_PLAIN:  beta = 1.
+ * SSD_INPUT_CONVEX: beta = 1 - a, so that h is a weighted mean of what came in.
+ * SSD_INPUT_UNIT:   beta = sqrt(1 - a^2), which keeps the variance of h at
+ *                   that of an uncorrelated input.
+ */
+typedef enum { SSD_INPUT_PLAIN = 0, SSD_INPUT_CONVEX = 1, SSD_INPUT_UNIT = 2 } ssd_input_scale;
+
+/*
+ * ssd_gated_scan -- the recurrence over whole sequences.
+ *
+ *   x, A_proj [B,H,N,d_h] dtype   input; decay logits A_P
+ *   I_proj    [B,H,N,d_h] dtype   input-gate logits I_P, or NULL: g = 1
+ *   initial_state [B,H,d_h] f32   in, optional (NULL = zero): h before token 0
+ *   d_h                           any >= 1 (a multiple of 4 takes wide accesses)
+ *   input_scale                   ssd_input_scale
+ *   y         [B,H,N,d_h] f32     out: h_t
+ *   final_state [B,H,d_h] f32     out, optional: h after token N-1 (with N = 0
+ *                                 the initial state or zero)
+ *   workspace                     >= ssd_gated_scan_workspace_size bytes
+ *
+ * Decays, states and sums are fp32.  The result does not depend on the
+ * workspace's contents, and the same call gives the same bits every time.
+ */
+size_t ssd_gated_scan_workspace_size(int64_t B, int64_t H, int64_t N, int64_t d_h);
+ssd_status ssd_gated_scan(const void* x, const void* A_proj, const void* I_proj,
+                          const float* initial_state, int64_t B, int64_t H, int64_t N, int64_t d_h,
+                          int input_scale, int dtype, float* y, float* final_state,
+                          void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * ssd_gated_scan_step -- one token for each of S sequences.
+ *
+ *   x, A_proj, I_proj [S,H,d_h] dtype (I_proj may be NULL)
+ *   state     [S,H,d_h] f32   h before the token
+ *   new_state [S,H,d_h] f32   out: h after it, which is also the step's y.
+ *                             May be `state` itself (the step in place); any
+ *                             other overlap is SSD_ERR_ALIAS.
+ */
+ssd_status ssd_gated_scan_step(const void* x, const void* A_proj, const void* I_proj,
+                               const float* state, int64_t S, int64_t H, int64_t d_h,
+                               int input_scale, int dtype, float* new_state, hipStream_t stream);
+
+/*
+ * ssd_gated_scan_backward -- gradients of ssd_gated_scan:
+ *     lam_t = dy_t + a_{t+1} lam_{t+1}   (the last token also + d_final_state)
+ *     dx = lam beta g,  dI_P = lam beta x g (1 - g),
+ *     dA_P = lam (beta' g x - a (1 - a) h_{t-1}),  d_initial_state = a_0 lam_0
+ * with beta' = d beta / d A_P = 0, a (1 - a) or a^2 sqrt((1 - a) / (1 + a)).
+ *
+ *   x, A_proj, I_proj, initial_state, B..dtype   as given to ssd_gated_scan
+ *   y  [B,H,N,d_h] f32              its output
+ *   dy [B,H,N,d_h] f32              gradient with respect to y
+ *   d_final_state [B,H,d_h] f32     gradient with respect to final_state, or NULL (zero)
+ *   dx, dA_proj, dI_proj [B,H,N,d_h] f32  out; dI_proj NULL iff I_proj is NULL
+ *   d_initial_state [B,H,d_h] f32   out, optional
+ *   workspace                       >= ssd_gated_scan_backward_workspace_size bytes
+ */
+size_t ssd_gated_scan_backward_workspace_size(int64_t B, int64_t H, int64_t N, int64_t d_h);
+ssd_status ssd_gated_scan_backward(const void* x, const void* A_proj, const void* I_proj,
+                                   const float* initial_state, const float* y, const float* dy,
+                                   const float* d_final_state, int64_t B, int64_t H, int64_t N,
+                                   int64_t d_h, int input_scale, int dtype, float* dx,
+                                   float* dA_proj, float* dI_proj, float* d_initial_state,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The two ends of a mixer block: the residual stream's side (ssd_norm_in, in
+ * front of the projections to q, k, v, dt, Z) and the output projection's side
+ * (ssd_norm_out).  Algorithm 3 computes the gate Z = h W_z; its use, the norms
+ * and the residual are not on the pages, and are taken as RMS norms with a
+ * weight per channel, a SiLU gate and a residual scale per channel.
+ * Outgoing gradients are f32, as ssd_backward's; an incoming gradient has the
+ * type of its array.  eps >= 0; with eps = 0 a row of zeros gives NaN, as the
+ * quotient does.  Sums of squares and gradient sums are fp32; the weight
+ * gradients are summed over rows in a fixed order (deterministic).
+ *
+ * ssd_norm_in -- what the previous block's output projection made is scaled
+ * and added to the residual stream, whose RMS norm is the next block's input:
+ *     r'_e = r_e + s_e p_e,   u_e = w_e r'_e / sqrt(mean_e r'^2 + eps)
+ *
+ *   residual     [rows,E] f32     r
+ *   branch       [rows,E] dtype   p, or NULL: r' = r, and residual_out must be NULL
+ *   branch_scale [E] f32          s, or NULL: 1 (must be NULL without branch)
+ *   weight       [E] f32          w
+ *   E                             1 .. SSD_NORM_MAX
+ *   residual_out [rows,E] f32     out: r'
+ *   out          [rows,E] dtype   out: u
+ */
+#define SSD_NORM_MAX 32768
+ssd_status ssd_norm_in(const float* residual, const void* branch, const float* branch_scale,
+                       const float* weight, int64_t rows, int64_t E, float eps, int dtype,
+                       float* residual_out, void* out, hipStream_t stream);
+
+/*
+ * ssd_norm_in_backward -- with c = du w, k = 1 / sqrt(mean r'^2 + eps):
+ *     dr = dr' + k c - k^3 mean(c r') r',   dp = s dr,
+ *     dw = sum over rows of du r' k,        ds = sum over rows of dr p
+ *
+ *   d_out          [rows,E] dtype  du
+ *   d_residual_out [rows,E] f32    dr', or NULL (zero)
+ *   residual_out   [rows,E] f32    r' (the input r of a call without branch)
+ *   branch, branch_scale           p and s, or both NULL: dp is then dr
+ *   d_residual     [rows,E] f32    out: dr
+ *   d_branch       [rows,E] f32    out: dp;  d_branch_scale [E] f32 out: ds
+ *                                  (both NULL iff branch_scale is NULL)
+ *   d_weight       [E] f32         out: dw
+ *   workspace                      >= ssd_norm_in_backward_workspace_size bytes
+ * With rows = 0 the two sums are written as zero.
+ */
+size_t ssd_norm_in_backward_workspace_size(int64_t rows, int64_t E);
+ssd_status ssd_norm_in_backward(const void* d_out, const float* d_residual_out,
+                                const float* residual_out, const void* branch,
+                                const float* branch_scale, const float* weight, int64_t rows,
+                                int64_t E, float eps, int dtype, float* d_residual,
+                                float* d_branch, float* d_weight, float* d_branch_scale,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * ssd_norm_out -- the mixer's y, gated by Z and normalised, from head order to
+ * token order.  Channel e = h d_h + c; the channels of a token form `groups`
+ * groups of H d_h / groups, each normalised for itself:
+ *   gate_first 1:  t = y silu(z),  o = w t / sqrt(mean_group t^2 + eps)
+ *   gate_first 0:  o = w silu(z) y / sqrt(mean_group y^2 + eps)
+ *
+ *   y      [B,H,N,d_h] f32     as ssd_forward and ssd_gated_scan write it
+ *                              (a decode step's [S,H,d_h]: B = S, N = 1)
+ *   z      [B,N,H d_h] dtype   gate logits Z
+ *   weight [H d_h] f32         w
+ *   groups                     a divisor of H (1: the whole token, H: each head);
+ *                              H d_h / groups <= SSD_NORM_MAX
+ *   out    [B,N,H d_h] dtype   out: o
+ */
+ssd_status ssd_norm_out(const float* y, const void* z, const float* weight, int64_t B, int64_t H,
+                        int64_t N, int64_t d_h, int64_t groups, int gate_first, float eps,
+                        int dtype, void* out, hipStream_t stream);
+
+/*
+ * ssd_norm_out_backward -- with k = 1 / sqrt(mean_group t^2 + eps), t = y silu(z):
+ *   gate_first 1:  dt = k do w - k^3 mean_group(do w t) t,
+ *                  dy = dt silu(z),  dz = dt y silu'(z),  dw = sum do t k
+ *   gate_first 0:  (t = y)  c = do w silu(z),  dy = k c - k^3 mean_group(c y) y,
+ *                  dz = do w y k silu'(z),  dw = sum do y k silu(z)
+ *
+ *   d_out     [B,N,H d_h] dtype  do
+ *   dy        [B,H,N,d_h] f32    out (as ssd_backward and ssd_gated_scan_backward take it)
+ *   dz        [B,N,H d_h] f32    out
+ *   d_weight  [H d_h] f32        out: the sum over b, n (zero when B N = 0)
+ *   workspace                    >= ssd_norm_out_backward_workspace_size bytes
+ */
+size_t ssd_norm_out_backward_workspace_size(int64_t B, int64_t H, int64_t N, int64_t d_h,
+                                            int64_t groups);
+ssd_status ssd_norm_out_backward(const void* d_out, const float* y, const void* z,
+                                 const float* weight, int64_t B, int64_t H, int64_t N, int64_t d_h,
+                                 int64_t groups, int gate_first, float eps, int dtype, float* dy,
+                                 float* dz, float* d_weight, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,6 +8,7 @@
 
 #include <mutex>
 
+#include "block.h"
 #include "bwd.h"
 #include "launch.h"
 
@@ -698,6 +699,327 @@ ssd_status ssd_prep_amask_backward(const float* A_proj, const float* dt_proj, co
                       "prep amask backward launch");
   } catch (...) {
     return fail(SSD_ERR_HIP, "ssd_prep_amask_backward: unexpected exception");
+  }
+}
+
+// ---- the gated linear recurrence ----
+
+// shared size validation; count = S H d_h or B H N d_h
+static ssd_status gated_sizes(const char* fn, int64_t B, int64_t H, int64_t N, int64_t d_h,
+                              int64_t* BH, int64_t* count) {
+  int64_t BHN;
+  if (d_h < 1 || !mul_ok(B, H, BH) || !mul_ok(*BH, N, &BHN) || !mul_ok(BHN, d_h, count))
+    return fail(SSD_ERR_SHAPE, "%s: sizes must be >= 0, d_h >= 1, and their product must not overflow", fn);
+  int64_t wide, slabs;  // a grid holds a workgroup per head, 16 channels and 64 tokens at most
+  if (!mul_ok(*BH, (d_h + 15) / 16, &slabs) || !mul_ok(slabs, (N + 63) / 64 + 1, &wide) ||
+      wide > (int64_t)0x7fffffff)
+    return fail(SSD_ERR_SHAPE, "%s: grid too large", fn);
+  return SSD_OK;
+}
+
+static ssd_status gated_kinds(const char* fn, int input_scale, int dtype) {
+  if (input_scale != SSD_INPUT_PLAIN && input_scale != SSD_INPUT_CONVEX && input_scale != SSD_INPUT_UNIT)
+    return fail(SSD_ERR_UNSUPPORTED, "%s: input_scale %d (0, 1 or 2)", fn, input_scale);
+  if (dtype != SSD_F32 && dtype != SSD_BF16) return fail(SSD_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
+  return SSD_OK;
+}
+
+static ssd_status check_workspace(const char* fn, const void* workspace, size_t given, size_t need) {
+  if (given < need || (need && !workspace))
+    return fail(SSD_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                workspace ? given : (size_t)0);
+  return SSD_OK;
+}
+
+size_t ssd_gated_scan_workspace_size(int64_t B, int64_t H, int64_t N, int64_t d_h) {
+  int64_t BH, n;
+  if (gated_sizes("ssd_gated_scan_workspace_size", B, H, N, d_h, &BH, &n) != SSD_OK || n == 0) return 0;
+  return ssd::gated_scan_floats(BH, N, d_h) * sizeof(float);
+}
+
+ssd_status ssd_gated_scan(const void* x, const void* A_proj, const void* I_proj,
+                          const float* initial_state, int64_t B, int64_t H, int64_t N, int64_t d_h,
+                          int input_scale, int dtype, float* y, float* final_state,
+                          void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const char* fn = "ssd_gated_scan";
+  try {
+    clear_err();
+    int64_t BH, n;
+    ssd_status s = gated_sizes(fn, B, H, N, d_h, &BH, &n);
+    if (s != SSD_OK || (s = gated_kinds(fn, input_scale, dtype)) != SSD_OK) return s;
+    if (BH == 0) return SSD_OK;  // no heads: nothing to compute
+    const Range h0{"initial_state", initial_state, (size_t)(BH * d_h) * 4};
+    const Range hf{"final_state", final_state, (size_t)(BH * d_h) * 4};
+    if (n == 0) {  // no tokens: the final state is the initial one (or zero)
+      if (!final_state) return SSD_OK;
+      if ((s = check_aligned(&h0, 1)) != SSD_OK || (s = check_aligned(&hf, 1)) != SSD_OK) return s;
+      if ((s = check_alias(&hf, 1, &h0, 1)) != SSD_OK) return s;
+      return hip_status(ssd::launch_copy_or_zero(final_state, initial_state, BH * d_h, stream),
+                        "final-state copy launch");
+    }
+    if (!x || !A_proj || !y) return fail(SSD_ERR_NULL, "%s: a required pointer is NULL", fn);
+    const size_t need = ssd::gated_scan_floats(BH, N, d_h) * sizeof(float);
+    if ((s = check_workspace(fn, workspace, workspace_bytes, need)) != SSD_OK) return s;
+    const size_t bytes = (size_t)n * (dtype == SSD_BF16 ? 2 : 4);
+    const Range ins[] = {{"x", x, bytes}, {"A_proj", A_proj, bytes}, {"I_proj", I_proj, bytes}, h0};
+    const Range outs[] = {{"y", y, (size_t)n * 4}, hf, {"workspace", workspace, need}};
+    if ((s = check_aligned(ins, 4)) != SSD_OK || (s = check_aligned(outs, 3)) != SSD_OK) return s;
+    if ((s = check_alias(outs, 3, ins, 4)) != SSD_OK) return s;
+    return hip_status(ssd::launch_gated_scan(dtype == SSD_BF16, input_scale, x, A_proj, I_proj,
+                                             initial_state, BH, N, d_h, y, final_state,
+                                             static_cast<float*>(workspace), stream),
+                      "gated_scan launch");
+  } catch (...) {
+    return fail(SSD_ERR_HIP, "%s: unexpected exception", fn);
+  }
+}
+
+ssd_status ssd_gated_scan_step(const void* x, const void* A_proj, const void* I_proj,
+                               const float* state, int64_t S, int64_t H, int64_t d_h,
+                               int input_scale, int dtype, float* new_state, hipStream_t stream) {
+  const char* fn = "ssd_gated_scan_step";
+  try {
+    clear_err();
+    int64_t SH, n;
+    ssd_status s = gated_sizes(fn, S, H, 1, d_h, &SH, &n);
+    if (s != SSD_OK || (s = gated_kinds(fn, input_scale, dtype)) != SSD_OK) return s;
+    if (n == 0) return SSD_OK;  // no sequences or heads: nothing to compute
+    if (!x || !A_proj || !state || !new_state) return fail(SSD_ERR_NULL, "%s: a required pointer is NULL", fn);
+    const size_t bytes = (size_t)n * (dtype == SSD_BF16 ? 2 : 4);
+    const Range ins[] = {{"x", x, bytes}, {"A_proj", A_proj, bytes}, {"I_proj", I_proj, bytes},
+                         {"state", state, (size_t)n * 4}};
+    const Range out{"new_state", new_state, (size_t)n * 4};
+    if ((s = check_aligned(ins, 4)) != SSD_OK || (s = check_aligned(&out, 1)) != SSD_OK) return s;
+    // in place: state itself is the one input that the output may be
+    if ((s = check_alias(&out, 1, ins, state == new_state ? 3 : 4)) != SSD_OK) return s;
+    return hip_status(ssd::launch_gated_scan_step(dtype == SSD_BF16, input_scale, x, A_proj, I_proj, state,
+                                                  n, new_state, stream),
+                      "gated_scan_step launch");
+  } catch (...) {
+    return fail(SSD_ERR_HIP, "%s: unexpected exception", fn);
+  }
+}
+
+size_t ssd_gated_scan_backward_workspace_size(int64_t B, int64_t H, int64_t N, int64_t d_h) {
+  int64_t BH, n;
+  if (gated_sizes("ssd_gated_scan_backward_workspace_size", B, H, N, d_h, &BH, &n) != SSD_OK || n == 0)
+    return 0;
+  return ssd::gated_scan_backward_floats(BH, N, d_h) * sizeof(float);
+}
+
+ssd_status ssd_gated_scan_backward(const void* x, const void* A_proj, const void* I_proj,
+                                   const float* initial_state, const float* y, const float* dy,
+                                   const float* d_final_state, int64_t B, int64_t H, int64_t N,
+                                   int64_t d_h, int input_scale, int dtype, float* dx,
+                                   float* dA_proj, float* dI_proj, float* d_initial_state,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const char* fn = "ssd_gated_scan_backward";
+  try {
+    clear_err();
+    int64_t BH, n;
+    ssd_status s = gated_sizes(fn, B, H, N, d_h, &BH, &n);
+    if (s != SSD_OK || (s = gated_kinds(fn, input_scale, dtype)) != SSD_OK) return s;
+    if (BH == 0) return SSD_OK;
+    const size_t st = (size_t)(BH * d_h) * 4;
+    const Range df{"d_final_state", d_final_state, st}, d0{"d_initial_state", d_initial_state, st};
+    if (n == 0) {  // no tokens: the state passes through
+      if (!d_initial_state) return SSD_OK;
+      if ((s = check_aligned(&df, 1)) != SSD_OK || (s = check_aligned(&d0, 1)) != SSD_OK) return s;
+      if ((s = check_alias(&d0, 1, &df, 1)) != SSD_OK) return s;
+      return hip_status(ssd::launch_copy_or_zero(d_initial_state, d_final_state, BH * d_h, stream),
+                        "initial-state gradient copy launch");
+    }
+    if (!x || !A_proj || !y || !dy || !dx || !dA_proj)
+      return fail(SSD_ERR_NULL, "%s: a required pointer is NULL", fn);
+    if ((I_proj == nullptr) != (dI_proj == nullptr))
+      return fail(SSD_ERR_NULL, "%s: I_proj and dI_proj must be given together", fn);
+    const size_t need = ssd::gated_scan_backward_floats(BH, N, d_h) * sizeof(float);
+    if ((s = check_workspace(fn, workspace, workspace_bytes, need)) != SSD_OK) return s;
+    const size_t bytes = (size_t)n * (dtype == SSD_BF16 ? 2 : 4), full = (size_t)n * 4;
+    const Range ins[] = {{"x", x, bytes},   {"A_proj", A_proj, bytes}, {"I_proj", I_proj, bytes},
+                         {"initial_state", initial_state, st},         {"y", y, full},
+                         {"dy", dy, full},  df};
+    const Range outs[] = {{"dx", dx, full}, {"dA_proj", dA_proj, full}, {"dI_proj", dI_proj, full}, d0,
+                          {"workspace", workspace, need}};
+    if ((s = check_aligned(ins, 7)) != SSD_OK || (s = check_aligned(outs, 5)) != SSD_OK) return s;
+    if ((s = check_alias(outs, 5, ins, 7)) != SSD_OK) return s;
+    return hip_status(ssd::launch_gated_scan_backward(dtype == SSD_BF16, input_scale, x, A_proj, I_proj,
+                                                      initial_state, y, dy, d_final_state, BH, N, d_h, dx,
+                                                      dA_proj, dI_proj, d_initial_state,
+                                                      static_cast<float*>(workspace), stream),
+                      "gated_scan_backward launch");
+  } catch (...) {
+    return fail(SSD_ERR_HIP, "%s: unexpected exception", fn);
+  }
+}
+
+// ---- the norms around a mixer block ----
+
+static ssd_status norm_kinds(const char* fn, int64_t E, float eps, int dtype) {
+  if (E < 1) return fail(SSD_ERR_SHAPE, "%s: a norm over %lld channels", fn, (long long)E);
+  if (E > SSD_NORM_MAX)
+    return fail(SSD_ERR_UNSUPPORTED, "%s: a norm over %lld channels (at most %d)", fn, (long long)E, SSD_NORM_MAX);
+  if (!(eps >= 0.f) || eps > 3.4028235e38f)
+    return fail(SSD_ERR_UNSUPPORTED, "%s: eps must be finite and >= 0", fn);
+  if (dtype != SSD_F32 && dtype != SSD_BF16) return fail(SSD_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
+  return SSD_OK;
+}
+
+static ssd_status norm_in_sizes(const char* fn, int64_t rows, int64_t E, int64_t* n) {
+  if (!mul_ok(rows, E, n)) return fail(SSD_ERR_SHAPE, "%s: rows must be >= 0 and rows E must not overflow", fn);
+  return SSD_OK;
+}
+
+ssd_status ssd_norm_in(const float* residual, const void* branch, const float* branch_scale,
+                       const float* weight, int64_t rows, int64_t E, float eps, int dtype,
+                       float* residual_out, void* out, hipStream_t stream) {
+  const char* fn = "ssd_norm_in";
+  try {
+    clear_err();
+    int64_t n;
+    ssd_status s = norm_kinds(fn, E, eps, dtype);
+    if (s != SSD_OK || (s = norm_in_sizes(fn, rows, E, &n)) != SSD_OK) return s;
+    if (n == 0) return SSD_OK;
+    if (!residual || !weight || !out) return fail(SSD_ERR_NULL, "%s: a required pointer is NULL", fn);
+    if ((branch == nullptr) != (residual_out == nullptr))
+      return fail(SSD_ERR_NULL, "%s: branch and residual_out must be given together", fn);
+    if (branch_scale && !branch) return fail(SSD_ERR_NULL, "%s: branch_scale without branch", fn);
+    const size_t bytes = (size_t)n * (dtype == SSD_BF16 ? 2 : 4);
+    const Range ins[] = {{"residual", residual, (size_t)n * 4}, {"branch", branch, bytes},
+                         {"branch_scale", branch_scale, (size_t)E * 4}, {"weight", weight, (size_t)E * 4}};
+    const Range outs[] = {{"residual_out", residual_out, (size_t)n * 4}, {"out", out, bytes}};
+    if ((s = check_aligned(ins, 4)) != SSD_OK || (s = check_aligned(outs, 2)) != SSD_OK) return s;
+    if ((s = check_alias(outs, 2, ins, 4)) != SSD_OK) return s;
+    return hip_status(ssd::launch_norm_in(dtype == SSD_BF16, residual, branch, branch_scale, weight, rows, E,
+                                          eps, residual_out, out, stream),
+                      "norm_in launch");
+  } catch (...) {
+    return fail(SSD_ERR_HIP, "%s: unexpected exception", fn);
+  }
+}
+
+size_t ssd_norm_in_backward_workspace_size(int64_t rows, int64_t E) {
+  int64_t n;
+  if (E < 1 || E > SSD_NORM_MAX ||
+      norm_in_sizes("ssd_norm_in_backward_workspace_size", rows, E, &n) != SSD_OK || n == 0)
+    return 0;
+  return ssd::norm_in_backward_floats(rows, E) * sizeof(float);
+}
+
+ssd_status ssd_norm_in_backward(const void* d_out, const float* d_residual_out,
+                                const float* residual_out, const void* branch,
+                                const float* branch_scale, const float* weight, int64_t rows,
+                                int64_t E, float eps, int dtype, float* d_residual,
+                                float* d_branch, float* d_weight, float* d_branch_scale,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const char* fn = "ssd_norm_in_backward";
+  try {
+    clear_err();
+    int64_t n;
+    ssd_status s = norm_kinds(fn, E, eps, dtype);
+    if (s != SSD_OK || (s = norm_in_sizes(fn, rows, E, &n)) != SSD_OK) return s;
+    if (!weight || !d_weight || (n && (!d_out || !residual_out || !d_residual)))
+      return fail(SSD_ERR_NULL, "%s: a required pointer is NULL", fn);
+    if ((branch_scale == nullptr) != (d_branch_scale == nullptr) ||
+        (n && ((branch_scale == nullptr) != (branch == nullptr) ||
+               (branch_scale == nullptr) != (d_branch == nullptr))))
+      return fail(SSD_ERR_NULL, "%s: branch, branch_scale, d_branch and d_branch_scale go together", fn);
+    const size_t need = n ? ssd::norm_in_backward_floats(rows, E) * sizeof(float) : 0;
+    if ((s = check_workspace(fn, workspace, workspace_bytes, need)) != SSD_OK) return s;
+    const size_t bytes = (size_t)n * (dtype == SSD_BF16 ? 2 : 4), full = (size_t)n * 4, ch = (size_t)E * 4;
+    const Range ins[] = {{"d_out", d_out, bytes},   {"d_residual_out", d_residual_out, full},
+                         {"residual_out", residual_out, full},      {"branch", branch, bytes},
+                         {"branch_scale", branch_scale, ch},        {"weight", weight, ch}};
+    const Range outs[] = {{"d_residual", d_residual, full}, {"d_branch", d_branch, full},
+                          {"d_weight", d_weight, ch},       {"d_branch_scale", d_branch_scale, ch},
+                          {"workspace", workspace, need}};
+    if ((s = check_aligned(ins, 6)) != SSD_OK || (s = check_aligned(outs, 5)) != SSD_OK) return s;
+    if ((s = check_alias(outs, 5, ins, 6)) != SSD_OK) return s;
+    return hip_status(ssd::launch_norm_in_backward(dtype == SSD_BF16, d_out, d_residual_out, residual_out,
+                                                   branch, branch_scale, weight, rows, E, eps, d_residual,
+                                                   d_branch, d_weight, d_branch_scale,
+                                                   static_cast<float*>(workspace), stream),
+                      "norm_in_backward launch");
+  } catch (...) {
+    return fail(SSD_ERR_HIP, "%s: unexpected exception", fn);
+  }
+}
+
+// sizes of both norm_out calls; n = B H N d_h, E = H d_h
+static ssd_status norm_out_sizes(const char* fn, int64_t B, int64_t H, int64_t N, int64_t d_h,
+                                 int64_t groups, int64_t* n, int64_t* E) {
+  int64_t BN, units;
+  if (H < 1 || d_h < 1 || groups < 1 || H % groups != 0)
+    return fail(SSD_ERR_SHAPE, "%s: H, d_h and groups must be >= 1 and groups must divide H", fn);
+  if (!mul_ok(B, N, &BN) || !mul_ok(H, d_h, E) || !mul_ok(BN, *E, n) || !mul_ok(BN, groups, &units))
+    return fail(SSD_ERR_SHAPE, "%s: B, N must be >= 0 and the product of the sizes must not overflow", fn);
+  return SSD_OK;
+}
+
+ssd_status ssd_norm_out(const float* y, const void* z, const float* weight, int64_t B, int64_t H,
+                        int64_t N, int64_t d_h, int64_t groups, int gate_first, float eps,
+                        int dtype, void* out, hipStream_t stream) {
+  const char* fn = "ssd_norm_out";
+  try {
+    clear_err();
+    int64_t n, E;
+    ssd_status s = norm_out_sizes(fn, B, H, N, d_h, groups, &n, &E);
+    if (s != SSD_OK || (s = norm_kinds(fn, E / groups, eps, dtype)) != SSD_OK) return s;
+    if (gate_first != 0 && gate_first != 1)
+      return fail(SSD_ERR_UNSUPPORTED, "%s: gate_first %d (0 or 1)", fn, gate_first);
+    if (n == 0) return SSD_OK;
+    if (!y || !z || !weight || !out) return fail(SSD_ERR_NULL, "%s: a required pointer is NULL", fn);
+    const size_t bytes = (size_t)n * (dtype == SSD_BF16 ? 2 : 4);
+    const Range ins[] = {{"y", y, (size_t)n * 4}, {"z", z, bytes}, {"weight", weight, (size_t)E * 4}};
+    const Range o{"out", out, bytes};
+    if ((s = check_aligned(ins, 3)) != SSD_OK || (s = check_aligned(&o, 1)) != SSD_OK) return s;
+    if ((s = check_alias(&o, 1, ins, 3)) != SSD_OK) return s;
+    return hip_status(ssd::launch_norm_out(dtype == SSD_BF16, gate_first != 0, y, z, weight, B, H, N, d_h,
+                                           groups, eps, out, stream),
+                      "norm_out launch");
+  } catch (...) {
+    return fail(SSD_ERR_HIP, "%s: unexpected exception", fn);
+  }
+}
+
+size_t ssd_norm_out_backward_workspace_size(int64_t B, int64_t H, int64_t N, int64_t d_h,
+                                            int64_t groups) {
+  int64_t n, E;
+  if (norm_out_sizes("ssd_norm_out_backward_workspace_size", B, H, N, d_h, groups, &n, &E) != SSD_OK ||
+      E / groups > SSD_NORM_MAX || n == 0)
+    return 0;
+  return ssd::norm_out_backward_floats(B, H, N, d_h, groups) * sizeof(float);
+}
+
+ssd_status ssd_norm_out_backward(const void* d_out, const float* y, const void* z,
+                                 const float* weight, int64_t B, int64_t H, int64_t N, int64_t d_h,
+                                 int64_t groups, int gate_first, float eps, int dtype, float* dy,
+                                 float* dz, float* d_weight, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream) {
+  const char* fn = "ssd_norm_out_backward";
+  try {
+    clear_err();
+    int64_t n, E;
+    ssd_status s = norm_out_sizes(fn, B, H, N, d_h, groups, &n, &E);
+    if (s != SSD_OK || (s = norm_kinds(fn, E / groups, eps, dtype)) != SSD_OK) return s;
+    if (gate_first != 0 && gate_first != 1)
+      return fail(SSD_ERR_UNSUPPORTED, "%s: gate_first %d (0 or 1)", fn, gate_first);
+    if (!weight || !d_weight || (n && (!d_out || !y || !z || !dy || !dz)))
+      return fail(SSD_ERR_NULL, "%s: a required pointer is NULL", fn);
+    const size_t need = n ? ssd::norm_out_backward_floats(B, H, N, d_h, groups) * sizeof(float) : 0;
+    if ((s = check_workspace(fn, workspace, workspace_bytes, need)) != SSD_OK) return s;
+    const size_t bytes = (size_t)n * (dtype == SSD_BF16 ? 2 : 4), full = (size_t)n * 4, ch = (size_t)E * 4;
+    const Range ins[] = {{"d_out", d_out, bytes}, {"y", y, full}, {"z", z, bytes}, {"weight", weight, ch}};
+    const Range outs[] = {{"dy", dy, full}, {"dz", dz, full}, {"d_weight", d_weight, ch},
+                          {"workspace", workspace, need}};
+    if ((s = check_aligned(ins, 4)) != SSD_OK || (s = check_aligned(outs, 4)) != SSD_OK) return s;
+    if ((s = check_alias(outs, 4, ins, 4)) != SSD_OK) return s;
+    return hip_status(ssd::launch_norm_out_backward(dtype == SSD_BF16, gate_first != 0, d_out, y, z, weight, B,
+                                                    H, N, d_h, groups, eps, dy, dz, d_weight,
+                                                    static_cast<float*>(workspace), stream),
+                      "norm_out_backward launch");
+  } catch (...) {
+    return fail(SSD_ERR_HIP, "%s: unexpected exception", fn);
   }
 }
 

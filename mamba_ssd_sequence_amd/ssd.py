@@ -13,6 +13,16 @@ call fails, an exception is raised.
     state_p, norm_p = state_pack(state, norm_state)
     dq, dk, dv, ddt, da = backward(q, k, v, dt, a_cs, y, den, dy, order=2, chunk=64)
     d_dt_proj, d_dt_bias, d_A_log = prep_backward(dt_proj, dt_bias, A_log, da, ddt)
+
+The gated linear recurrence, and the norms, gate and residual scale around a mixer block:
+
+    y = gated_scan(x, A_proj, I_proj, scale=SSD_INPUT_UNIT)
+    state = gated_scan_step(x, A_proj, I_proj, state, scale=SSD_INPUT_UNIT)
+    dx, dA_proj, dI_proj, dh0 = gated_scan_backward(x, A_proj, I_proj, y, dy, scale=SSD_INPUT_UNIT)
+    residual, u = norm_in(residual, branch, branch_scale, weight, eps)
+    d_residual, d_branch, d_weight, d_scale = norm_in_backward(du, d_residual, residual, branch, branch_scale, weight, eps)
+    o = norm_out(y, z, weight, eps, groups=1, gate_first=True)
+    dy, dz, d_weight = norm_out_backward(do, y, z, weight, eps, groups=1, gate_first=True)
 """
 from __future__ import annotations
 
@@ -29,6 +39,9 @@ SSD_F32 = 0
 SSD_BF16 = 1
 SSD_STATE_FULL = 0
 SSD_STATE_PACKED = 1
+SSD_INPUT_PLAIN = 0
+SSD_INPUT_CONVEX = 1
+SSD_INPUT_UNIT = 2
 SSD_NOALLOC_SCRATCH_BYTES = 64 << 20  # include/ssd.h
 STATUS = ["SSD_OK", "SSD_ERR_NULL", "SSD_ERR_SHAPE", "SSD_ERR_UNSUPPORTED", "SSD_ERR_ALIGN",
           "SSD_ERR_ALIAS", "SSD_ERR_WORKSPACE", "SSD_ERR_HIP"]
@@ -87,6 +100,31 @@ def _declare(lib):
     lib.ssd_prep_backward.argtypes = [fp, fp, fp, fp, fp, i64, i64, i64, fp, fp, fp, vp]
     lib.ssd_prep_amask_backward.restype = ctypes.c_int
     lib.ssd_prep_amask_backward.argtypes = [fp, fp, fp, fp, i64, i64, i64, fp, fp, vp]
+    f32 = ctypes.c_float
+    lib.ssd_gated_scan_workspace_size.restype = sz
+    lib.ssd_gated_scan_workspace_size.argtypes = [i64, i64, i64, i64]
+    lib.ssd_gated_scan.restype = ctypes.c_int
+    lib.ssd_gated_scan.argtypes = [vp, vp, vp, fp, i64, i64, i64, i64, i32, i32, fp, fp, vp, sz, vp]
+    lib.ssd_gated_scan_step.restype = ctypes.c_int
+    lib.ssd_gated_scan_step.argtypes = [vp, vp, vp, fp, i64, i64, i64, i32, i32, fp, vp]
+    lib.ssd_gated_scan_backward_workspace_size.restype = sz
+    lib.ssd_gated_scan_backward_workspace_size.argtypes = [i64, i64, i64, i64]
+    lib.ssd_gated_scan_backward.restype = ctypes.c_int
+    lib.ssd_gated_scan_backward.argtypes = [vp, vp, vp, fp, fp, fp, fp, i64, i64, i64, i64, i32, i32,
+                                            fp, fp, fp, fp, vp, sz, vp]
+    lib.ssd_norm_in.restype = ctypes.c_int
+    lib.ssd_norm_in.argtypes = [fp, vp, fp, fp, i64, i64, f32, i32, fp, vp, vp]
+    lib.ssd_norm_in_backward_workspace_size.restype = sz
+    lib.ssd_norm_in_backward_workspace_size.argtypes = [i64, i64]
+    lib.ssd_norm_in_backward.restype = ctypes.c_int
+    lib.ssd_norm_in_backward.argtypes = [vp, fp, fp, vp, fp, fp, i64, i64, f32, i32, fp, fp, fp, fp, vp, sz, vp]
+    lib.ssd_norm_out.restype = ctypes.c_int
+    lib.ssd_norm_out.argtypes = [fp, vp, fp, i64, i64, i64, i64, i64, i32, f32, i32, vp, vp]
+    lib.ssd_norm_out_backward_workspace_size.restype = sz
+    lib.ssd_norm_out_backward_workspace_size.argtypes = [i64, i64, i64, i64, i64]
+    lib.ssd_norm_out_backward.restype = ctypes.c_int
+    lib.ssd_norm_out_backward.argtypes = [vp, fp, vp, fp, i64, i64, i64, i64, i64, i32, f32, i32, fp, fp, fp,
+                                          vp, sz, vp]
     return lib
 
 
@@ -426,3 +464,198 @@ def prep_amask_backward(A_proj, dt_proj, da, ddt=None):
     _check(lib().ssd_prep_amask_backward(_ptr(A_proj), opt(dt_proj), _ptr(da), opt(ddt), B, H, N,
                                          _ptr(d_A), opt(d_dt), _stream(dev)))
     return d_A, d_dt
+
+
+# ---- the gated linear recurrence and the norms around a mixer block ----
+
+
+def _gpu(named, dtypes, device, shapes):
+    """Checks of a call's tensors: (name, tensor or None) pairs on one device,
+    contiguous, of the given types and shapes."""
+    for (name, t), dtype, shape in zip(named, dtypes, shapes):
+        if t is not None:
+            _require(t, name, dtype, device)
+            if t.shape != shape:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _call(fn, device, *args):
+    """fn(*args, stream) on the arrays' device and its current stream (the
+    library launches on the current device)."""
+    torch = _torch()
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(device)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(device)))
+
+
+def _scratch(workspace, need, device):
+    """(pointer, bytes, tensor) of a call's workspace; one is allocated when None is given."""
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+    else:
+        _require(workspace, "workspace", None, device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def gated_scan(x, A_proj, I_proj=None, *, scale: int, initial_state=None, final_state=None, y=None,
+               workspace=None):
+    """ssd_gated_scan: h_t = a_t h_{t-1} + beta_t g_t x_t with a = sigmoid(-A_proj), g = sigmoid(I_proj)
+    (or 1) and beta by scale (SSD_INPUT_PLAIN, _CONVEX, _UNIT).  x, A_proj, I_proj [B,H,N,d_h] bf16 or
+    fp32, states [B,H,d_h] fp32 (final_state is written when given); returns y [B,H,N,d_h] fp32."""
+    torch = _torch()
+    _require(x, "x")
+    dev, shape, f32 = x.device, x.shape, torch.float32
+    dtype = _qkv_dtype(x)
+    B, H, N, d_h = shape
+    if y is None:
+        y = torch.empty(shape, dtype=f32, device=dev)
+    _gpu((("A_proj", A_proj), ("I_proj", I_proj), ("initial_state", initial_state),
+          ("final_state", final_state), ("y", y)), (x.dtype, x.dtype, f32, f32, f32), dev,
+         (shape, shape, (B, H, d_h), (B, H, d_h), shape))
+    ws, wbytes, keep = _scratch(workspace, lib().ssd_gated_scan_workspace_size(B, H, N, d_h), dev)
+    _call(lib().ssd_gated_scan, dev, _addr(x), _addr(A_proj), _addr(I_proj), _addr(initial_state), B, H, N, d_h,
+          scale, dtype, _addr(y), _addr(final_state), ws, wbytes)
+    return y
+
+
+def gated_scan_step(x, A_proj, I_proj, state, *, scale: int, new_state=None):
+    """ssd_gated_scan_step: one token of S sequences, x, A_proj, I_proj (or None) [S,H,d_h], state
+    [S,H,d_h] fp32.  The state is updated in place unless new_state is given; returns the new state,
+    which is the step's output."""
+    torch = _torch()
+    _require(x, "x")
+    dev, shape, f32 = x.device, x.shape, torch.float32
+    dtype = _qkv_dtype(x)
+    S, H, d_h = shape
+    if new_state is None:
+        new_state = state
+    _gpu((("A_proj", A_proj), ("I_proj", I_proj), ("state", state), ("new_state", new_state)),
+         (x.dtype, x.dtype, f32, f32), dev, (shape, shape, shape, shape))
+    _call(lib().ssd_gated_scan_step, dev, _addr(x), _addr(A_proj), _addr(I_proj), _addr(state), S, H, d_h, scale,
+          dtype, _addr(new_state))
+    return new_state
+
+
+def gated_scan_backward(x, A_proj, I_proj, y, dy, *, scale: int, initial_state=None, d_final_state=None,
+                        workspace=None):
+    """ssd_gated_scan_backward: returns dx, dA_proj, dI_proj (None without I_proj) and d_initial_state
+    (None without initial_state), all fp32.  y: gated_scan's output; dy, d_final_state (or None): the
+    gradients with respect to y and the final state."""
+    torch = _torch()
+    _require(x, "x")
+    dev, shape, f32 = x.device, x.shape, torch.float32
+    dtype = _qkv_dtype(x)
+    B, H, N, d_h = shape
+    _gpu((("A_proj", A_proj), ("I_proj", I_proj), ("y", y), ("dy", dy), ("initial_state", initial_state),
+          ("d_final_state", d_final_state)), (x.dtype, x.dtype, f32, f32, f32, f32), dev,
+         (shape, shape, shape, shape, (B, H, d_h), (B, H, d_h)))
+    dx, dA = torch.empty_like(y), torch.empty_like(y)
+    dI = torch.empty_like(y) if I_proj is not None else None
+    dh0 = torch.empty_like(initial_state) if initial_state is not None else None
+    ws, wbytes, keep = _scratch(workspace, lib().ssd_gated_scan_backward_workspace_size(B, H, N, d_h), dev)
+    _call(lib().ssd_gated_scan_backward, dev, _addr(x), _addr(A_proj), _addr(I_proj), _addr(initial_state),
+          _addr(y), _addr(dy), _addr(d_final_state), B, H, N, d_h, scale, dtype, _addr(dx), _addr(dA), _addr(dI),
+          _addr(dh0), ws, wbytes)
+    return dx, dA, dI, dh0
+
+
+def norm_in(residual, branch, branch_scale, weight, eps: float, *, dtype=None, residual_out=None, out=None):
+    """ssd_norm_in: r' = residual + branch_scale branch, u = weight r' / sqrt(mean r'^2 + eps) over the last
+    dimension.  residual [..,E] fp32; branch [..,E] bf16 or fp32, or None (then r' is residual, and dtype
+    is u's type); branch_scale [E] fp32 or None (1).  Returns (r' fp32, u of branch's type)."""
+    torch = _torch()
+    f32 = torch.float32
+    _require(residual, "residual", f32)
+    dev, shape = residual.device, residual.shape
+    E = shape[-1]
+    if branch is not None:
+        dtype = branch.dtype
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    kind = _qkv_dtype(out)
+    _gpu((("branch", branch), ("branch_scale", branch_scale), ("weight", weight), ("residual_out", residual_out),
+          ("out", out)), (out.dtype, f32, f32, f32, dtype), dev, (shape, (E,), (E,), shape, shape))
+    rows = residual.numel() // E if E else 0
+    _call(lib().ssd_norm_in, dev, _addr(residual), _addr(branch), _addr(branch_scale), _addr(weight), rows, E, eps,
+          kind, _addr(residual_out), _addr(out))
+    return (residual if branch is None else residual_out), out
+
+
+def norm_in_backward(d_out, d_residual_out, residual_out, branch, branch_scale, weight, eps: float, *,
+                     workspace=None):
+    """ssd_norm_in_backward: returns d_residual [..,E], d_branch [..,E], d_weight [E], d_branch_scale [E], all
+    fp32.  Without branch_scale the branch's gradient is d_residual itself and d_branch_scale is None; branch
+    is then not read.  d_residual_out: fp32, or None (zero); residual_out: the r' of norm_in."""
+    torch = _torch()
+    f32 = torch.float32
+    _require(d_out, "d_out")
+    dev, shape = d_out.device, d_out.shape
+    kind = _qkv_dtype(d_out)
+    E = shape[-1]
+    if branch_scale is not None and branch is None:
+        raise ValueError("branch_scale without branch")
+    if branch_scale is None:
+        branch = None
+    _gpu((("d_residual_out", d_residual_out), ("residual_out", residual_out), ("branch", branch),
+          ("branch_scale", branch_scale), ("weight", weight)), (f32, f32, d_out.dtype, f32, f32), dev,
+         (shape, shape, shape, (E,), (E,)))
+    rows = d_out.numel() // E if E else 0
+    d_residual = torch.empty_like(residual_out)
+    d_weight = torch.empty_like(weight)
+    d_branch = torch.empty_like(residual_out) if branch is not None else None
+    d_scale = torch.empty_like(weight) if branch is not None else None
+    ws, wbytes, keep = _scratch(workspace, lib().ssd_norm_in_backward_workspace_size(rows, E), dev)
+    _call(lib().ssd_norm_in_backward, dev, _addr(d_out), _addr(d_residual_out), _addr(residual_out), _addr(branch),
+          _addr(branch_scale), _addr(weight), rows, E, eps, kind, _addr(d_residual), _addr(d_branch),
+          _addr(d_weight), _addr(d_scale), ws, wbytes)
+    return d_residual, (d_residual if d_branch is None else d_branch), d_weight, d_scale
+
+
+def norm_out(y, z, weight, eps: float, *, groups: int = 1, gate_first: bool = True, out=None):
+    """ssd_norm_out: the mixer's y [B,H,N,d_h] fp32, gated by silu(z) and normalised over `groups` groups of a
+    token's channels, in token order: z and the result [B,N,H d_h] bf16 or fp32, weight [H d_h] fp32."""
+    torch = _torch()
+    f32 = torch.float32
+    _require(y, "y", f32)
+    _require(z, "z", None, y.device)
+    dev = y.device
+    B, H, N, d_h = y.shape
+    shape = (B, N, H * d_h)
+    kind = _qkv_dtype(z)
+    if out is None:
+        out = torch.empty(shape, dtype=z.dtype, device=dev)
+    _gpu((("z", z), ("weight", weight), ("out", out)), (z.dtype, f32, z.dtype), dev, (shape, (H * d_h,), shape))
+    _call(lib().ssd_norm_out, dev, _addr(y), _addr(z), _addr(weight), B, H, N, d_h, groups, 1 if gate_first else 0,
+          eps, kind, _addr(out))
+    return out
+
+
+def norm_out_backward(d_out, y, z, weight, eps: float, *, groups: int = 1, gate_first: bool = True,
+                      workspace=None):
+    """ssd_norm_out_backward: returns dy [B,H,N,d_h], dz [B,N,H d_h], d_weight [H d_h], all fp32."""
+    torch = _torch()
+    f32 = torch.float32
+    _require(y, "y", f32)
+    _require(z, "z", None, y.device)
+    dev = y.device
+    B, H, N, d_h = y.shape
+    shape = (B, N, H * d_h)
+    kind = _qkv_dtype(z)
+    _gpu((("d_out", d_out), ("z", z), ("weight", weight)), (z.dtype, z.dtype, f32), dev,
+         (shape, shape, (H * d_h,)))
+    dy, d_weight = torch.empty_like(y), torch.empty_like(weight)
+    dz = torch.empty(shape, dtype=f32, device=dev)
+    ws, wbytes, keep = _scratch(workspace, lib().ssd_norm_out_backward_workspace_size(B, H, N, d_h, groups), dev)
+    _call(lib().ssd_norm_out_backward, dev, _addr(d_out), _addr(y), _addr(z), _addr(weight), B, H, N, d_h, groups,
+          1 if gate_first else 0, eps, kind, _addr(dy), _addr(dz), _addr(d_weight), ws, wbytes)
+    return dy, dz, d_weight

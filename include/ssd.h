@@ -413,13 +413,16 @@ ssd_status ssd_prep_amask_backward(const float* A_proj, const float* dt_proj, co
  */
 typedef enum { SSD_INPUT_PLAIN = 0, SSD_INPUT_CONVEX = 1, SSD_INPUT_UNIT = 2 } ssd_input_scale;
 
+/* The largest d_h of the recurrence. */
+#define SSD_GATED_MAX (1 << 20)
+
 /*
  * ssd_gated_scan -- the recurrence over whole sequences.
  *
  *   x, A_proj [B,H,N,d_h] dtype   input; decay logits A_P
  *   I_proj    [B,H,N,d_h] dtype   input-gate logits I_P, or NULL: g = 1
  *   initial_state [B,H,d_h] f32   in, optional (NULL = zero): h before token 0
- *   d_h                           any >= 1 (a multiple of 4 takes wide accesses)
+ *   d_h                           1 .. SSD_GATED_MAX (a multiple of 4 takes wide accesses)
  *   input_scale                   ssd_input_scale
  *   y         [B,H,N,d_h] f32     out: h_t
  *   final_state [B,H,d_h] f32     out, optional: h after token N-1 (with N = 0
@@ -427,7 +430,9 @@ typedef enum { SSD_INPUT_PLAIN = 0, SSD_INPUT_CONVEX = 1, SSD_INPUT_UNIT = 2 } s
  *   workspace                     >= ssd_gated_scan_workspace_size bytes
  *
  * Decays, states and sums are fp32.  The result does not depend on the
- * workspace's contents, and the same call gives the same bits every time.
+ * workspace's contents, and the same call gives the same bits every time.  A
+ * workspace serves one call at a time: calls that may overlap (other streams,
+ * graphs replayed at once) take one each.
  */
 size_t ssd_gated_scan_workspace_size(int64_t B, int64_t H, int64_t N, int64_t d_h);
 ssd_status ssd_gated_scan(const void* x, const void* A_proj, const void* I_proj,

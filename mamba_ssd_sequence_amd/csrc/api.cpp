@@ -710,6 +710,8 @@ static ssd_status gated_sizes(const char* fn, int64_t B, int64_t H, int64_t N, i
   int64_t BHN;
   if (d_h < 1 || !mul_ok(B, H, BH) || !mul_ok(*BH, N, &BHN) || !mul_ok(BHN, d_h, count))
     return fail(SSD_ERR_SHAPE, "%s: sizes must be >= 0, d_h >= 1, and their product must not overflow", fn);
+  if (d_h > SSD_GATED_MAX)
+    return fail(SSD_ERR_UNSUPPORTED, "%s: d_h %lld (at most %d)", fn, (long long)d_h, SSD_GATED_MAX);
   int64_t wide, slabs;  // a grid holds a workgroup per head, 16 channels and 64 tokens at most
   if (!mul_ok(*BH, (d_h + 15) / 16, &slabs) || !mul_ok(slabs, (N + 63) / 64 + 1, &wide) ||
       wide > (int64_t)0x7fffffff)

@@ -61,53 +61,407 @@ __device__ __forceinline__ void decay_of(float A, float& a, float& rest, float& 
   }
 }
 
-// One thread per channel, a token after the other.
-template <typename T, int SCALE>
-__global__ __launch_bounds__(64) void k_gated_scan(const T* __restrict__ x, const T* __restrict__ A,
-                                                   const T* __restrict__ I,
-                                                   const float* __restrict__ h0, int64_t N,
-                                                   int64_t DH, int64_t slabs, float* __restrict__ y,
-                                                   float* __restrict__ hf) {
-  const int64_t bh = blockIdx.x / slabs;
-  const int64_t c = (blockIdx.x - bh * slabs) * 64 + threadIdx.x;
-  if (c >= DH) return;
-  float h = h0 ? h0[bh * DH + c] : 0.f;
-  int64_t at = bh * N * DH + c;
-  for (int64_t t = 0; t < N; ++t, at += DH) {
-    float a, rest, beta, db;
-    decay_of<SCALE>(Elem<T>::ld(A, at), a, rest, beta, db);
-    const float g = I ? sigmoid_v(Elem<T>::ld(I, at)) : 1.f;
-    h = fmaf(a, h, beta * g * Elem<T>::ld(x, at));
-    y[at] = h;
-  }
-  if (hf) hf[bh * DH + c] = h;
+// ---- whole sequences ----
+//
+// One workgroup takes a tile: TILE consecutive tokens of C channels of one
+// head, read once, held in registers as decays and inputs, and written once.
+// Lane l of a wave owns V channels (l % LPR) of TT consecutive tokens (its
+// group l / LPR); groups, then waves, follow each other along the tokens.
+//  1. Each thread composes its TT steps h -> a h + u to one step (P, U); the
+//     wave scans its groups' steps by lane shuffles, the waves' steps go to LDS.
+//  2. The first wave, a lane per channel, composes them to the tile's step,
+//     publishes it, waits for the steps of the earlier tiles of the same span
+//     of SPAN tiles and for the state that enters the span, and so has the
+//     state entering the tile and each wave.
+//  3. Every thread runs its tokens from its own entering state and writes y.
+// The alternative, a pass over the inputs for the segments' steps and a second
+// one for the outputs, reads x, A_P and I_P twice.
+//
+// Waiting.  A workgroup takes the next tile of its head from a counter, so the
+// tiles before its own belong to workgroups that have started; each publishes
+// its tile's step before it waits for anything.  The state entering a span is
+// published by the last tile of the span before, after waits on steps and on
+// the state entering that span: by induction from the first span, which waits
+// for no state, every wait ends, in whatever order workgroups are scheduled.
+// A published value is one 8-byte word of the float and a mark, stored and read
+// by relaxed atomics of the whole device: the word itself says whether it is
+// there, so no fence (a write-back of the XCD's L2) is needed.  Counters and
+// words are cleared by a kernel in front.
+// The order of every composition is fixed by the sizes alone, so the same call
+// gives the same bits.
+
+constexpr int SPAN = 32;
+
+typedef unsigned long long word_t;
+
+__device__ __forceinline__ void put_word(word_t* p, float v) {
+  __hip_atomic_store(p, ((word_t)1 << 32) | __float_as_uint(v), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
 }
 
-template <typename T, int SCALE>
-__global__ __launch_bounds__(64) void k_gated_scan_bwd(
+__device__ __forceinline__ word_t get_word(const word_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ bool is_there(word_t w) { return (w >> 32) != 0; }
+__device__ __forceinline__ float value_of(word_t w) { return __uint_as_float((unsigned)w); }
+
+// V consecutive elements of a row as they are stored; forget(): what was
+// computed from them is not kept for later use
+template <typename T, int V> struct Raw;
+template <> struct Raw<uint16_t, 4> {
+  uint2 r;
+  __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r.x), "+v"(r.y)); }
+  __device__ __forceinline__ void load(const uint16_t* p) { r = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ float get(int v) const {
+    const unsigned w = v < 2 ? r.x : r.y;
+    return __uint_as_float(v % 2 ? w & 0xffff0000u : w << 16);
+  }
+};
+template <> struct Raw<float, 4> {
+  f32x4 r;
+  __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
+  __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const f32x4*>(p); }
+  __device__ __forceinline__ float get(int v) const { return r[v]; }
+};
+template <> struct Raw<uint16_t, 1> {
+  uint16_t r;
+  __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
+  __device__ __forceinline__ void load(const uint16_t* p) { r = *p; }
+  __device__ __forceinline__ float get(int) const { return bf16_to_f32(r); }
+};
+template <> struct Raw<float, 1> {
+  float r;
+  __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
+  __device__ __forceinline__ void load(const float* p) { r = *p; }
+  __device__ __forceinline__ float get(int) const { return r; }
+};
+
+template <int V>
+__device__ __forceinline__ void store_row(float* p, const float (&v)[V]) {
+  if constexpr (V == 4)
+    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+  else
+    *p = v[0];
+}
+
+// The shape of a tile.  NW waves; TT tokens a thread.
+template <int V_, int LPR_, int NW_, int TT_>
+struct Tile {
+  static constexpr int V = V_, LPR = LPR_, NW = NW_, TT = TT_;
+  static constexpr int TG = WAVE / LPR;       // groups of a wave
+  static constexpr int C = LPR * V;           // channels
+  static constexpr int TOKENS = NW * TG * TT;
+};
+
+// Words and counters of the tiles of one channel slab of one head, `tiles` > 1:
+// [tiles][2][C] words (P, U), [spans][C] words (state entering the span).
+__host__ __device__ inline int64_t span_count(int64_t tiles) { return (tiles + SPAN - 1) / SPAN; }
+__host__ __device__ inline int64_t slab_words(int64_t tiles, int C) {
+  return (tiles * 2 + span_count(tiles)) * C;
+}
+
+__global__ __launch_bounds__(256) void k_clear_words(uint4* p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    p[i] = make_uint4(0, 0, 0, 0);
+}
+
+// Steps (P, U) of the groups of a wave along its tokens (reverse: from the last
+// group to the first) -> for each group the composition of the groups before it;
+// the whole wave's composition goes to LDS.
+template <typename TL, bool REVERSE>
+__device__ __forceinline__ void scan_groups(float (&P)[TL::V], float (&U)[TL::V], int lane, float* sP,
+                                            float* sU) {
+  const int tg = REVERSE ? TL::TG - 1 - lane / TL::LPR : lane / TL::LPR;
+  auto before = [](float x, int groups) {
+    return REVERSE ? __shfl_down(x, groups * TL::LPR, WAVE) : __shfl_up(x, groups * TL::LPR, WAVE);
+  };
+#pragma unroll
+  for (int o = 1; o < TL::TG; o <<= 1)
+#pragma unroll
+    for (int v = 0; v < TL::V; ++v) {
+      const float p = before(P[v], o), u = before(U[v], o);
+      if (tg >= o) {
+        U[v] = fmaf(P[v], u, U[v]);
+        P[v] *= p;
+      }
+    }
+  if (tg == TL::TG - 1) {
+    const int c = lane % TL::LPR * TL::V;
+    store_row<TL::V>(sP + c, P);
+    store_row<TL::V>(sU + c, U);
+  }
+#pragma unroll
+  for (int v = 0; v < TL::V; ++v) {
+    const float p = before(P[v], 1), u = before(U[v], 1);
+    P[v] = tg ? p : 1.f;
+    U[v] = tg ? u : 0.f;
+  }
+}
+
+// The first wave's part, a lane per channel: from the waves' steps in LDS to
+// the state entering each wave (sH), by way of the other tiles.  `order`: the
+// tile's place in the scan's direction; `first`: the state entering the whole
+// sequence (read by the tiles of the first span).
+template <typename TL, bool REVERSE>
+__device__ __forceinline__ void join_tiles(const float* sP, const float* sU, float* sH, int c,
+                                            int order, int tiles, float first, word_t* words) {
+  constexpr int C = TL::C, NW = TL::NW;
+  float P = 1.f, U = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < NW; ++i) {
+    const int at = (REVERSE ? NW - 1 - i : i) * C + c;
+    U = fmaf(sP[at], U, sU[at]);
+    P *= sP[at];
+  }
+  float h = first;
+  if (tiles > 1) {
+    const int span = order / SPAN;
+    word_t* states = words + (int64_t)tiles * 2 * C + c;
+    words += c;
+    if (order % SPAN != SPAN - 1 && order + 1 < tiles) {  // someone may read the tile's step
+      put_word(words + (int64_t)order * 2 * C, P);
+      put_word(words + ((int64_t)order * 2 + 1) * C, U);
+    }
+    if (span) {
+      word_t s;
+      while (!is_there(s = get_word(states + (int64_t)span * C))) __builtin_amdgcn_s_sleep(1);
+      h = value_of(s);
+    }
+    constexpr int BATCH = 4;  // steps waited for at once
+    for (int t = span * SPAN; t < order; t += BATCH) {
+      word_t p[BATCH], u[BATCH];
+      bool all;
+      do {
+        all = true;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int64_t at = t + i < order ? t + i : t;
+          p[i] = get_word(words + at * 2 * C);
+          u[i] = get_word(words + (at * 2 + 1) * C);
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) all = all && is_there(p[i]) && is_there(u[i]);
+      } while (!all);
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i)
+        if (t + i < order) h = fmaf(value_of(p[i]), h, value_of(u[i]));
+    }
+    if (order % SPAN == SPAN - 1 && order + 1 < tiles)
+      put_word(states + ((int64_t)span + 1) * C, fmaf(P, h, U));
+  }
+#pragma unroll 4
+  for (int i = 0; i < NW; ++i) {
+    const int at = (REVERSE ? NW - 1 - i : i) * C + c;
+    sH[at] = h;
+    h = fmaf(sP[at], h, sU[at]);
+  }
+}
+
+// the next tile of this workgroup's head (in the scan's order)
+__device__ __forceinline__ int take_tile(int tiles, unsigned* counter) {
+  if (tiles == 1) return 0;
+  __shared__ unsigned mine;
+  if (threadIdx.x == 0)
+    mine = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(mine);
+}
+
+// Where a workgroup and a thread are: every array is addressed from a uniform
+// pointer at the tile's first row by 32-bit offsets (at most 512 rows of at most
+// SSD_GATED_MAX = 2^20 channels), so that offsets past 2^32 elements cost no
+// registers.
+template <typename TL>
+struct Spot {
+  int64_t base, state;  // element of the tile's first row and channel; of the head's state
+  int tok, rows, c;     // the thread's first token in the tile, the tile's tokens, its channel
+  bool live;            // the channel exists
+  __device__ __forceinline__ Spot(int64_t hs, int tile, int64_t N, int DH, int slabs) {
+    const int64_t bh = hs / slabs;
+    const int slab = (int)(hs - bh * slabs), lane = threadIdx.x % WAVE;
+    const int64_t left = N - (int64_t)tile * TL::TOKENS;
+    rows = left < TL::TOKENS ? (int)left : TL::TOKENS;
+    state = bh * DH + slab * TL::C;
+    base = (bh * N + (int64_t)tile * TL::TOKENS) * DH + slab * TL::C;
+    tok = (threadIdx.x / WAVE * TL::TG + lane / TL::LPR) * TL::TT;
+    c = lane % TL::LPR * TL::V;
+    live = slab * TL::C + c < DH;
+    if (!live) c = 0;
+  }
+  // offset of row tok + i, or of the last row
+  __device__ __forceinline__ unsigned at(int i, int DH) const {
+    return (unsigned)(tok + i < rows ? tok + i : rows - 1) * (unsigned)DH + (unsigned)c;
+  }
+};
+
+template <typename T, int SCALE, bool GATE, typename TL>
+__global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan(
+    const T* __restrict__ x, const T* __restrict__ A, const T* __restrict__ I,
+    const float* __restrict__ h0, int64_t N, int DH, int slabs, int heads, int tiles,
+    float* __restrict__ y, float* __restrict__ hf, unsigned* counters, word_t* words) {
+  constexpr int V = TL::V, TT = TL::TT, C = TL::C;
+  __shared__ float sP[TL::NW * C], sU[TL::NW * C], sH[TL::NW * C];
+  const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+  const int hs = blockIdx.x % heads;  // head and slab
+  const int tile = take_tile(tiles, counters + hs);
+  const Spot<TL> sp(hs, tile, N, DH, slabs);
+  x += sp.base;
+  A += sp.base;
+  I += sp.base;
+  y += sp.base;
+
+  Raw<T, V> rx[TT], rA[TT], rI[TT];
+#pragma unroll
+  for (int i = 0; i < TT; ++i) {
+    const unsigned at = sp.at(i, DH);
+    rA[i].load(A + at);
+    if constexpr (GATE) rI[i].load(I + at);
+    rx[i].load(x + at);
+  }
+  float a[TT][V], u[TT][V], P[V], U[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    P[v] = 1.f;
+    U[v] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < TT; ++i) {
+    const bool in = sp.tok + i < sp.rows;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      // tokens past the end leave the state alone: a = 1, x = 0
+      float rest, beta, db;
+      decay_of<SCALE>(in ? rA[i].get(v) : -INFINITY, a[i][v], rest, beta, db);
+      float g = 1.f;
+      if constexpr (GATE) g = sigmoid_v(rI[i].get(v));
+      u[i][v] = beta * g * (in ? rx[i].get(v) : 0.f);
+      U[v] = fmaf(a[i][v], U[v], u[i][v]);
+      P[v] *= a[i][v];
+    }
+  }
+  scan_groups<TL, false>(P, U, lane, sP + wave * C, sU + wave * C);
+  __syncthreads();
+  if (wave == 0 && lane < C && hs % slabs * C + lane < DH)
+    join_tiles<TL, false>(sP, sU, sH, lane, tile, tiles, h0 ? h0[sp.state + lane] : 0.f,
+                          words + hs * slab_words(tiles, C));
+  __syncthreads();
+  float h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = fmaf(P[v], sH[wave * C + sp.c + v], U[v]);
+  const bool last = tile == tiles - 1 && hf;
+#pragma unroll
+  for (int i = 0; i < TT; ++i) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], u[i][v]);
+    if (sp.live && sp.tok + i < sp.rows) {
+      store_row<V>(y + sp.at(i, DH), h);
+      if (last && sp.tok + i == sp.rows - 1) store_row<V>(hf + sp.state + sp.c, h);
+    }
+  }
+}
+
+// The gradients: the same tiles from the last token to the first, with the
+// state c_t = a_t lam_t, c_t = a_t (dy_t + c_{t+1}), c_N = d_final_state and
+// lam_t = dy_t + c_{t+1}; c_0 is the gradient of the initial state.  Only A_P
+// and dy are needed for a tile's step; x, I_P and the states before each token
+// (y one token earlier) are read when the tile's entering c is known.
+template <typename T, int SCALE, bool GATE, typename TL>
+__global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
     const T* __restrict__ x, const T* __restrict__ A, const T* __restrict__ I,
     const float* __restrict__ h0, const float* __restrict__ y, const float* __restrict__ dy,
-    const float* __restrict__ dlast, int64_t N, int64_t DH, int64_t slabs, float* __restrict__ dx,
-    float* __restrict__ dA, float* __restrict__ dI, float* __restrict__ dh0) {
-  const int64_t bh = blockIdx.x / slabs;
-  const int64_t c = (blockIdx.x - bh * slabs) * 64 + threadIdx.x;
-  if (c >= DH) return;
-  float carry = dlast ? dlast[bh * DH + c] : 0.f;  // a_{t+1} lam_{t+1}
-  int64_t at = (bh * N + N - 1) * DH + c;
-  for (int64_t t = N - 1; t >= 0; --t, at -= DH) {
-    float a, rest, beta, db;
-    decay_of<SCALE>(Elem<T>::ld(A, at), a, rest, beta, db);
-    const float g = I ? sigmoid_v(Elem<T>::ld(I, at)) : 1.f;
-    const float xv = Elem<T>::ld(x, at);
-    const float prev = t ? y[at - DH] : (h0 ? h0[bh * DH + c] : 0.f);
-    const float lam = dy[at] + carry;
-    dx[at] = lam * beta * g;
-    dA[at] = lam * (db * g * xv - a * rest * prev);
-    if (dI) dI[at] = lam * beta * xv * g * (1.f - g);
-    carry = a * lam;
+    const float* __restrict__ dlast, int64_t N, int DH, int slabs, int heads, int tiles,
+    float* __restrict__ dx, float* __restrict__ dA, float* __restrict__ dI,
+    float* __restrict__ dh0, unsigned* counters, word_t* words) {
+  constexpr int V = TL::V, TT = TL::TT, C = TL::C;
+  __shared__ float sP[TL::NW * C], sU[TL::NW * C], sH[TL::NW * C];
+  const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+  const int hs = blockIdx.x % heads;
+  const int order = take_tile(tiles, counters + hs), tile = tiles - 1 - order;
+  const Spot<TL> sp(hs, tile, N, DH, slabs);
+  x += sp.base;
+  A += sp.base;
+  I += sp.base;
+  dy += sp.base;
+  y += sp.base - DH;  // a row before the tile: the states before each token
+  dx += sp.base;
+  dA += sp.base;
+  dI += sp.base;
+  const bool first = tile == 0 && sp.tok == 0;  // the sequence's first token: the state before it is h0
+
+  Raw<T, V> rA[TT], rx[TT], rI[TT];
+  Raw<float, V> rd[TT], rp[TT], r0;
+#pragma unroll
+  for (int i = 0; i < TT; ++i) {
+    rA[i].load(A + sp.at(i, DH));
+    rd[i].load(dy + sp.at(i, DH));
   }
-  if (dh0) dh0[bh * DH + c] = carry;
+#pragma unroll
+  for (int i = 0; i < TT; ++i) {
+    const unsigned at = sp.at(i, DH);
+    rx[i].load(x + at);
+    if constexpr (GATE) rI[i].load(I + at);
+    // the row before; before the sequence's first row there is none, and its own is read without use
+    rp[i].load(y + (tile == 0 && at < (unsigned)DH ? at + DH : at));
+  }
+  if (tile == 0 && h0) r0.load(h0 + sp.state + sp.c);
+  float P[V], U[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    P[v] = 1.f;
+    U[v] = 0.f;
+  }
+#pragma unroll
+  for (int i = TT - 1; i >= 0; --i)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const bool in = sp.tok + i < sp.rows;  // tokens past the end: a = 1, dy = 0
+      float a, rest;
+      sigmoid_pair(in ? rA[i].get(v) : -INFINITY, rest, a);
+      U[v] = a * ((in ? rd[i].get(v) : 0.f) + U[v]);
+      P[v] *= a;
+    }
+  scan_groups<TL, true>(P, U, lane, sP + wave * C, sU + wave * C);
+  __syncthreads();
+  if (wave == 0 && lane < C && hs % slabs * C + lane < DH)
+    join_tiles<TL, true>(sP, sU, sH, lane, order, tiles, dlast ? dlast[sp.state + lane] : 0.f,
+                         words + hs * slab_words(tiles, C));
+  __syncthreads();
+  // the decays are computed again rather than held over the wait
+#pragma unroll
+  for (int i = 0; i < TT; ++i) rA[i].forget();
+  float carry[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) carry[v] = fmaf(P[v], sH[wave * C + sp.c + v], U[v]);
+#pragma unroll
+  for (int i = TT - 1; i >= 0; --i) {
+    if (!sp.live || sp.tok + i >= sp.rows) continue;
+    float ox[V], oA[V], oI[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float a, rest, beta, db, g = 1.f;
+      decay_of<SCALE>(rA[i].get(v), a, rest, beta, db);
+      const float lam = rd[i].get(v) + carry[v], xv = rx[i].get(v);
+      if constexpr (GATE) {
+        float ng;
+        sigmoid_pair(rI[i].get(v), g, ng);
+        oI[v] = lam * beta * xv * g * ng;
+      }
+      float prev = rp[i].get(v);
+      if (i == 0 && first) prev = h0 ? r0.get(v) : 0.f;
+      ox[v] = lam * beta * g;
+      oA[v] = lam * (SCALE == IN_PLAIN ? -(a * rest) * prev : fmaf(db * g, xv, -(a * rest) * prev));
+      carry[v] = a * lam;
+    }
+    const unsigned at = sp.at(i, DH);
+    store_row<V>(dx + at, ox);
+    store_row<V>(dA + at, oA);
+    if constexpr (GATE) store_row<V>(dI + at, oI);
+    if (i == 0 && first && dh0) store_row<V>(dh0 + sp.state + sp.c, carry);
+  }
 }
+
+// ---- single tokens ----
 
 template <typename T, int SCALE>
 __global__ __launch_bounds__(256) void k_gated_step(const T* __restrict__ x, const T* __restrict__ A,
@@ -120,9 +474,6 @@ __global__ __launch_bounds__(256) void k_gated_step(const T* __restrict__ x, con
   const float g = I ? sigmoid_v(Elem<T>::ld(I, i)) : 1.f;
   out[i] = fmaf(a, state[i], beta * g * Elem<T>::ld(x, i));
 }
-
-size_t gated_scan_floats(int64_t, int64_t, int64_t) { return 0; }
-size_t gated_scan_backward_floats(int64_t, int64_t, int64_t) { return 0; }
 
 // calls f<T, SCALE>()
 template <typename F>
@@ -137,14 +488,79 @@ static hipError_t by_type(bool bf16, int scale, F&& f) {
   return bf16 ? with(uint16_t{}) : with(float{});
 }
 
+// The tile of a call: 4 channels a lane where rows are whole 16-byte (bf16:
+// 8-byte) pieces, d_h a multiple of 4, 64 channels a tile (32 when the head has
+// no more); else a channel a lane, 16 a tile.
+enum { WIDE64, WIDE32, NARROW };
+static int tile_kind(int64_t DH) { return DH % 4 ? NARROW : DH > 32 ? WIDE64 : WIDE32; }
+constexpr int kind_lpr(int k) { return k == WIDE32 ? 8 : 16; }
+constexpr int kind_v(int k) { return k == NARROW ? 1 : 4; }
+
+constexpr int FWD_WAVES = 8, BWD_WAVES = 8;
+constexpr int fwd_tokens(bool bf16) { return bf16 ? 8 : 4; }
+constexpr int BWD_TOKENS = 4;
+
+struct Split {
+  int64_t slabs, heads, tiles;
+  int C;
+  // floats: the counters, padded, then the words
+  size_t counters() const { return (size_t)((heads + 63) & ~(int64_t)63); }
+  size_t floats() const { return tiles > 1 ? counters() + (size_t)(heads * slab_words(tiles, C)) * 2 : 0; }
+};
+
+static Split split_of(int64_t BH, int64_t N, int64_t DH, int waves, int tokens) {
+  const int k = tile_kind(DH), lpr = kind_lpr(k), C = lpr * kind_v(k);
+  const int64_t slabs = (DH + C - 1) / C, per = (int64_t)waves * (WAVE / lpr) * tokens;
+  return {slabs, BH * slabs, (N + per - 1) / per, C};
+}
+
+// for either element type
+size_t gated_scan_floats(int64_t BH, int64_t N, int64_t DH) {
+  const size_t a = split_of(BH, N, DH, FWD_WAVES, fwd_tokens(true)).floats();
+  const size_t b = split_of(BH, N, DH, FWD_WAVES, fwd_tokens(false)).floats();
+  return a > b ? a : b;
+}
+
+size_t gated_scan_backward_floats(int64_t BH, int64_t N, int64_t DH) {
+  return split_of(BH, N, DH, BWD_WAVES, BWD_TOKENS).floats();
+}
+
+static hipError_t clear_words(const Split& s, float* ws, hipStream_t stream) {
+  const int64_t n = (int64_t)((s.floats() + 3) / 4), want = (n + 255) / 256;
+  if (!n) return hipSuccess;
+  hipLaunchKernelGGL(k_clear_words, dim3((unsigned)(want < 256 ? want : 256)), dim3(256), 0, stream,
+                     (uint4*)ws, n);
+  return hipGetLastError();
+}
+
+// calls f(T, SCALE, GATE, kind) with types for the call's element type, scale, gate and tile
+template <typename F>
+static hipError_t by_call(bool bf16, int scale, bool gate, int64_t DH, F&& f) {
+  return by_type(bf16, scale, [&](auto t, auto sc) {
+    auto with = [&](auto g) {
+      switch (tile_kind(DH)) {
+        case WIDE64: return f(t, sc, g, std::integral_constant<int, WIDE64>{});
+        case WIDE32: return f(t, sc, g, std::integral_constant<int, WIDE32>{});
+        default: return f(t, sc, g, std::integral_constant<int, NARROW>{});
+      }
+    };
+    return gate ? with(std::true_type{}) : with(std::false_type{});
+  });
+}
+
 hipError_t launch_gated_scan(bool bf16, int scale, const void* x, const void* A, const void* I,
                              const float* h0, int64_t BH, int64_t N, int64_t DH, float* y,
-                             float* hf, float*, hipStream_t stream) {
-  const int64_t slabs = (DH + 63) / 64;
-  return by_type(bf16, scale, [&](auto t, auto sc) {
+                             float* hf, float* ws, hipStream_t stream) {
+  const Split s = split_of(BH, N, DH, FWD_WAVES, fwd_tokens(bf16));
+  const hipError_t e = clear_words(s, ws, stream);
+  if (e != hipSuccess) return e;
+  return by_call(bf16, scale, I != nullptr, DH, [&](auto t, auto sc, auto g, auto k) {
     using T = decltype(t);
-    hipLaunchKernelGGL((k_gated_scan<T, sc.value>), dim3((unsigned)(BH * slabs)), dim3(64), 0, stream,
-                       (const T*)x, (const T*)A, (const T*)I, h0, N, DH, slabs, y, hf);
+    using TL = Tile<kind_v(k.value), kind_lpr(k.value), FWD_WAVES, fwd_tokens(sizeof(T) == 2)>;
+    hipLaunchKernelGGL((k_gated_scan<T, sc.value, g.value, TL>), dim3((unsigned)(s.heads * s.tiles)),
+                       dim3(TL::NW * WAVE), 0, stream, (const T*)x, (const T*)A, (const T*)I, h0, N,
+                       (int)DH, (int)s.slabs, (int)s.heads, (int)s.tiles, y, hf, (unsigned*)ws,
+                       (word_t*)(ws + s.counters()));
     return hipGetLastError();
   });
 }
@@ -164,13 +580,17 @@ hipError_t launch_gated_scan_backward(bool bf16, int scale, const void* x, const
                                       const void* I, const float* h0, const float* y,
                                       const float* dy, const float* dlast, int64_t BH, int64_t N,
                                       int64_t DH, float* dx, float* dA, float* dI, float* dh0,
-                                      float*, hipStream_t stream) {
-  const int64_t slabs = (DH + 63) / 64;
-  return by_type(bf16, scale, [&](auto t, auto sc) {
+                                      float* ws, hipStream_t stream) {
+  const Split s = split_of(BH, N, DH, BWD_WAVES, BWD_TOKENS);
+  const hipError_t e = clear_words(s, ws, stream);
+  if (e != hipSuccess) return e;
+  return by_call(bf16, scale, I != nullptr, DH, [&](auto t, auto sc, auto g, auto k) {
     using T = decltype(t);
-    hipLaunchKernelGGL((k_gated_scan_bwd<T, sc.value>), dim3((unsigned)(BH * slabs)), dim3(64), 0,
-                       stream, (const T*)x, (const T*)A, (const T*)I, h0, y, dy, dlast, N, DH, slabs,
-                       dx, dA, dI, dh0);
+    using TL = Tile<kind_v(k.value), kind_lpr(k.value), BWD_WAVES, BWD_TOKENS>;
+    hipLaunchKernelGGL((k_gated_scan_bwd<T, sc.value, g.value, TL>), dim3((unsigned)(s.heads * s.tiles)),
+                       dim3(TL::NW * WAVE), 0, stream, (const T*)x, (const T*)A, (const T*)I, h0, y, dy,
+                       dlast, N, (int)DH, (int)s.slabs, (int)s.heads, (int)s.tiles, dx, dA, dI, dh0,
+                       (unsigned*)ws, (word_t*)(ws + s.counters()));
     return hipGetLastError();
   });
 }

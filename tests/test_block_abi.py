@@ -30,6 +30,7 @@ def test_scan_errors(lib):
         assert scan(lib, **bad) == 2, bad
     assert scan(lib, scale=3) == 3 and scan(lib, scale=-1) == 3
     assert scan(lib, dtype=2) == 3
+    assert scan(lib, H=1, N=1, d=(1 << 20) + 1) == 3
     for name in ("x", "Ap", "Ip", "y", "h0", "hf", "ws"):
         assert scan(lib, **{name: A[8] + 4}) == 4, name
     assert scan(lib, y=A[0]) == 5 and scan(lib, y=A[2] + 64) == 5

@@ -955,6 +955,8 @@ static ssd_status norm_out_sizes(const char* fn, int64_t B, int64_t H, int64_t N
     return fail(SSD_ERR_SHAPE, "%s: H, d_h and groups must be >= 1 and groups must divide H", fn);
   if (!mul_ok(B, N, &BN) || !mul_ok(H, d_h, E) || !mul_ok(BN, *E, n) || !mul_ok(BN, groups, &units))
     return fail(SSD_ERR_SHAPE, "%s: B, N must be >= 0 and the product of the sizes must not overflow", fn);
+  if (BN > (int64_t)0x7fffffff || *E > (int64_t)0x7fffffff)
+    return fail(SSD_ERR_SHAPE, "%s: more than 2^31 - 1 tokens or channels", fn);
   return SSD_OK;
 }
 

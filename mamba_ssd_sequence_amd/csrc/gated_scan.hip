@@ -6,39 +6,11 @@
 //     lam_t = dy_t + a_{t+1} lam_{t+1}.
 #include "block.h"
 #include "common.h"
+#include "elem.h"
 
 #include <type_traits>
 
 namespace ssd {
-
-// e^x for x <= 0 to about 1.5 ulp: 2^(x log2 e) on the hardware exponential
-// with the rounding of the product and of log2 e put back to first order.
-// Below -104 the result is 0; NaN stays NaN.
-__device__ __forceinline__ float exp_neg(float x) {
-  x = x < -104.f ? -104.f : x;
-  const float t = x * LOG2E;
-  const float lo = fmaf(x, 1.925963033500011e-08f, fmaf(x, LOG2E, -t));  // x log2 e - t
-  const float e = exp2_fast(t);
-  return fmaf(e, lo * 0.6931471805599453f, e);
-}
-
-// sigmoid(x) and 1 - sigmoid(x) = sigmoid(-x).  The smaller of the two is
-// e / (1 + e) with e = e^{-|x|} and has its own relative accuracy; the larger
-// is one minus it, a single rounding: a decay near 1 is then right to half an
-// ulp, without the bias of a reciprocal that a thousand tokens would add up.
-__device__ __forceinline__ void sigmoid_pair(float x, float& s, float& rest) {
-  const float e = exp_neg(-fabsf(x));
-  const float small = e * __builtin_amdgcn_rcpf(1.f + e);
-  const float large = 1.f - small;
-  s = x > 0.f ? large : small;
-  rest = x > 0.f ? small : large;
-}
-
-__device__ __forceinline__ float sigmoid_v(float x) {
-  float s, rest;
-  sigmoid_pair(x, s, rest);
-  return s;
-}
 
 enum { IN_PLAIN = 0, IN_CONVEX = 1, IN_UNIT = 2 };
 
@@ -105,45 +77,6 @@ __device__ __forceinline__ word_t get_word(const word_t* p) {
 
 __device__ __forceinline__ bool is_there(word_t w) { return (w >> 32) != 0; }
 __device__ __forceinline__ float value_of(word_t w) { return __uint_as_float((unsigned)w); }
-
-// V consecutive elements of a row as they are stored; forget(): what was
-// computed from them is not kept for later use
-template <typename T, int V> struct Raw;
-template <> struct Raw<uint16_t, 4> {
-  uint2 r;
-  __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r.x), "+v"(r.y)); }
-  __device__ __forceinline__ void load(const uint16_t* p) { r = *reinterpret_cast<const uint2*>(p); }
-  __device__ __forceinline__ float get(int v) const {
-    const unsigned w = v < 2 ? r.x : r.y;
-    return __uint_as_float(v % 2 ? w & 0xffff0000u : w << 16);
-  }
-};
-template <> struct Raw<float, 4> {
-  f32x4 r;
-  __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
-  __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const f32x4*>(p); }
-  __device__ __forceinline__ float get(int v) const { return r[v]; }
-};
-template <> struct Raw<uint16_t, 1> {
-  uint16_t r;
-  __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
-  __device__ __forceinline__ void load(const uint16_t* p) { r = *p; }
-  __device__ __forceinline__ float get(int) const { return bf16_to_f32(r); }
-};
-template <> struct Raw<float, 1> {
-  float r;
-  __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
-  __device__ __forceinline__ void load(const float* p) { r = *p; }
-  __device__ __forceinline__ float get(int) const { return r; }
-};
-
-template <int V>
-__device__ __forceinline__ void store_row(float* p, const float (&v)[V]) {
-  if constexpr (V == 4)
-    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-  else
-    *p = v[0];
-}
 
 // The shape of a tile.  NW waves; TT tokens a thread.
 template <int V_, int LPR_, int NW_, int TT_>

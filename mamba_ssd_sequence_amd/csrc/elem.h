@@ -6,40 +6,41 @@
 
 namespace ssd {
 
-// e^x for x <= 0 to about 1.5 ulp: 2^(x log2 e) on the hardware exponential
-// with the rounding of the product and of log2 e put back to first order.
-// Below -104 the result is 0; NaN stays NaN.
-__device__ __forceinline__ float exp_neg(float x) {
-  x = x < -104.f ? -104.f : x;
-  const float t = x * LOG2E;
-  const float lo = fmaf(x, 1.925963033500011e-08f, fmaf(x, LOG2E, -t));  // x log2 e - t
-  const float e = exp2_fast(t);
-  return fmaf(e, lo * 0.6931471805599453f, e);
-}
+// e^x to (|x| + 3) roundings: 2^(x log2 e) on the hardware exponential (1 ulp),
+// whose argument is rounded once.  Infinities and NaN come out as e^x has them.
+// (Putting that rounding back to first order costs 4 more instructions; the
+// error it leaves is that of terms which e^{-|x|} has made small.)
+__device__ __forceinline__ float exp_fast(float x) { return exp2_fast(x * LOG2E); }
 
 // sigmoid(x) and 1 - sigmoid(x) = sigmoid(-x).  The smaller of the two is
 // e / (1 + e) with e = e^{-|x|} and has its own relative accuracy; the larger
 // is one minus it, a single rounding: a decay near 1 is then right to half an
 // ulp, without the bias of a reciprocal that a thousand tokens would add up.
 __device__ __forceinline__ void sigmoid_pair(float x, float& s, float& rest) {
-  const float e = exp_neg(-fabsf(x));
+  const float e = exp_fast(-fabsf(x));
   const float small = e * __builtin_amdgcn_rcpf(1.f + e);
   const float large = 1.f - small;
   s = x > 0.f ? large : small;
   rest = x > 0.f ? small : large;
 }
 
+// sigmoid(x) alone: 1 / (1 + e^{-x}), to a few roundings at either end (below
+// x = -88, where the result is under 1e-38, it is 0).
 __device__ __forceinline__ float sigmoid_v(float x) {
-  float s, rest;
-  sigmoid_pair(x, s, rest);
-  return s;
+  return __builtin_amdgcn_rcpf(1.f + exp_fast(-x));
 }
 
-// V consecutive elements of a row as they are stored; forget(): what was
-// computed from them is not kept for later use
+// V consecutive elements of a row as they are stored.  or_else(): the elements,
+// or one bit pattern for all of them (fp32's upper half) where `in` is false;
+// forget(): what was computed from them is not kept for later use.
 template <typename T, int V> struct Raw;
 template <> struct Raw<uint16_t, 4> {
   uint2 r;
+  __device__ __forceinline__ void or_else(bool in, unsigned other) {
+    other = other << 16 | other;
+    r.x = in ? r.x : other;
+    r.y = in ? r.y : other;
+  }
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r.x), "+v"(r.y)); }
   __device__ __forceinline__ void load(const uint16_t* p) { r = *reinterpret_cast<const uint2*>(p); }
   __device__ __forceinline__ float get(int v) const {
@@ -49,18 +50,24 @@ template <> struct Raw<uint16_t, 4> {
 };
 template <> struct Raw<float, 4> {
   f32x4 r;
+  __device__ __forceinline__ void or_else(bool in, unsigned other) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) r[v] = in ? r[v] : __uint_as_float(other << 16);
+  }
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
   __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const f32x4*>(p); }
   __device__ __forceinline__ float get(int v) const { return r[v]; }
 };
 template <> struct Raw<uint16_t, 1> {
   uint16_t r;
+  __device__ __forceinline__ void or_else(bool in, unsigned other) { r = in ? r : (uint16_t)other; }
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
   __device__ __forceinline__ void load(const uint16_t* p) { r = *p; }
   __device__ __forceinline__ float get(int) const { return bf16_to_f32(r); }
 };
 template <> struct Raw<float, 1> {
   float r;
+  __device__ __forceinline__ void or_else(bool in, unsigned other) { r = in ? r : __uint_as_float(other << 16); }
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
   __device__ __forceinline__ void load(const float* p) { r = *p; }
   __device__ __forceinline__ float get(int) const { return r; }

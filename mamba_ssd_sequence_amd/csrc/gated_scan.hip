@@ -14,9 +14,20 @@ namespace ssd {
 
 enum { IN_PLAIN = 0, IN_CONVEX = 1, IN_UNIT = 2 };
 
-// a, 1 - a, beta(a) and, for the backward pass, d beta / d A_P
+// a and beta(a) from the logit
 template <int SCALE>
-__device__ __forceinline__ void decay_of(float A, float& a, float& rest, float& beta, float& dbeta) {
+__device__ __forceinline__ void decay_of(float A, float& a, float& beta) {
+  float rest;
+  sigmoid_pair(A, rest, a);
+  if constexpr (SCALE == IN_PLAIN) beta = 1.f;
+  if constexpr (SCALE == IN_CONVEX) beta = rest;
+  // 1 - a^2 = (1 - a)(1 + a) without cancellation
+  if constexpr (SCALE == IN_UNIT) beta = __builtin_amdgcn_sqrtf(fmaf(rest, a, rest));
+}
+
+// a, 1 - a, beta and d beta / d A_P, for the gradients
+template <int SCALE>
+__device__ __forceinline__ void decay_slope(float A, float& a, float& rest, float& beta, float& dbeta) {
   sigmoid_pair(A, rest, a);
   if constexpr (SCALE == IN_PLAIN) {
     beta = 1.f;
@@ -25,8 +36,8 @@ __device__ __forceinline__ void decay_of(float A, float& a, float& rest, float& 
     beta = rest;
     dbeta = a * rest;
   } else {
-    // beta = sqrt(q), dbeta = a^2 (1 - a) / beta, q = 1 - a^2 without cancellation
-    const float q = rest * (1.f + a);
+    // beta = sqrt(q), dbeta = a^2 (1 - a) / beta (0 where a = 1), q = 1 - a^2
+    const float q = fmaf(rest, a, rest);
     const float inv = q == 0.f ? 0.f : __builtin_amdgcn_rsqf(q);
     beta = q * inv;
     dbeta = a * a * rest * inv;
@@ -41,10 +52,11 @@ __device__ __forceinline__ void decay_of(float A, float& a, float& rest, float& 
 // group l / LPR); groups, then waves, follow each other along the tokens.
 //  1. Each thread composes its TT steps h -> a h + u to one step (P, U); the
 //     wave scans its groups' steps by lane shuffles, the waves' steps go to LDS.
-//  2. The first wave, a lane per channel, composes them to the tile's step,
-//     publishes it, waits for the steps of the earlier tiles of the same span
-//     of SPAN tiles and for the state that enters the span, and so has the
-//     state entering the tile and each wave.
+//  2. The first wave, a lane per channel, composes them to the tile's step and
+//     publishes it.  The steps of the earlier tiles of the same span of SPAN
+//     tiles are read by all waves, some by each, and composed wave by wave; with
+//     the state that enters the span the first wave then has the state entering
+//     the tile and each of its waves.
 //  3. Every thread runs its tokens from its own entering state and writes y.
 // The alternative, a pass over the inputs for the segments' steps and a second
 // one for the outputs, reads x, A_P and I_P twice.
@@ -55,10 +67,12 @@ __device__ __forceinline__ void decay_of(float A, float& a, float& rest, float& 
 // published by the last tile of the span before, after waits on steps and on
 // the state entering that span: by induction from the first span, which waits
 // for no state, every wait ends, in whatever order workgroups are scheduled.
-// A published value is one 8-byte word of the float and a mark, stored and read
-// by relaxed atomics of the whole device: the word itself says whether it is
-// there, so no fence (a write-back of the XCD's L2) is needed.  Counters and
-// words are cleared by a kernel in front.
+// What is published is one 8-byte word a channel, stored and read by relaxed
+// atomics of the whole device: the word itself says whether it is there, so no
+// fence (a write-back of the XCD's L2) is needed.  A step's word holds P and U,
+// marked by P's sign bit (P is a product of decays in [0, 1], or NaN, whose sign
+// says nothing); a state's word holds the state and a mark.  Counters and words
+// are cleared by a kernel in front.
 // The order of every composition is fixed by the sizes alone, so the same call
 // gives the same bits.
 
@@ -66,8 +80,10 @@ constexpr int SPAN = 32;
 
 typedef unsigned long long word_t;
 
-__device__ __forceinline__ void put_word(word_t* p, float v) {
-  __hip_atomic_store(p, ((word_t)1 << 32) | __float_as_uint(v), __ATOMIC_RELAXED,
+constexpr unsigned MARK = 0x80000000u;
+
+__device__ __forceinline__ void put_word(word_t* p, unsigned hi, float lo) {
+  __hip_atomic_store(p, (word_t)hi << 32 | __float_as_uint(lo), __ATOMIC_RELAXED,
                      __HIP_MEMORY_SCOPE_AGENT);
 }
 
@@ -75,8 +91,9 @@ __device__ __forceinline__ word_t get_word(const word_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-__device__ __forceinline__ bool is_there(word_t w) { return (w >> 32) != 0; }
-__device__ __forceinline__ float value_of(word_t w) { return __uint_as_float((unsigned)w); }
+__device__ __forceinline__ bool is_there(word_t w) { return (w >> 63) != 0; }
+__device__ __forceinline__ float step_p(word_t w) { return __uint_as_float((unsigned)(w >> 32) & ~MARK); }
+__device__ __forceinline__ float low_value(word_t w) { return __uint_as_float((unsigned)w); }
 
 // The shape of a tile.  NW waves; TT tokens a thread.
 template <int V_, int LPR_, int NW_, int TT_>
@@ -88,10 +105,10 @@ struct Tile {
 };
 
 // Words and counters of the tiles of one channel slab of one head, `tiles` > 1:
-// [tiles][2][C] words (P, U), [spans][C] words (state entering the span).
+// [tiles][C] words (steps), [spans][C] words (states entering the spans).
 __host__ __device__ inline int64_t span_count(int64_t tiles) { return (tiles + SPAN - 1) / SPAN; }
 __host__ __device__ inline int64_t slab_words(int64_t tiles, int C) {
-  return (tiles * 2 + span_count(tiles)) * C;
+  return (tiles + span_count(tiles)) * C;
 }
 
 __global__ __launch_bounds__(256) void k_clear_words(uint4* p, int64_t n) {
@@ -132,63 +149,83 @@ __device__ __forceinline__ void scan_groups(float (&P)[TL::V], float (&U)[TL::V]
   }
 }
 
-// The first wave's part, a lane per channel: from the waves' steps in LDS to
-// the state entering each wave (sH), by way of the other tiles.  `order`: the
-// tile's place in the scan's direction; `first`: the state entering the whole
-// sequence (read by the tiles of the first span).
+// LDS of a workgroup: the steps of its waves, the composed steps of the earlier
+// tiles of the span (each wave's share), the states entering its waves.
+template <typename TL>
+struct Joint {
+  float P[TL::NW * TL::C], U[TL::NW * TL::C], spanP[TL::NW * TL::C], spanU[TL::NW * TL::C],
+      H[TL::NW * TL::C];
+};
+
+// From the waves' steps in LDS (complete) to the state entering each wave
+// (j.H, complete on return), by way of the other tiles; lane c < C of a wave is
+// channel c, `exists` says whether the head has it.  `order`: the tile's place
+// in the scan's direction; `first`: the state entering the whole sequence, in
+// the first wave's lanes.
 template <typename TL, bool REVERSE>
-__device__ __forceinline__ void join_tiles(const float* sP, const float* sU, float* sH, int c,
-                                            int order, int tiles, float first, word_t* words) {
-  constexpr int C = TL::C, NW = TL::NW;
+__device__ __forceinline__ void join_tiles(Joint<TL>& j, int wave, int c, bool exists, int order,
+                                           int tiles, float first, word_t* words) {
+  constexpr int C = TL::C, NW = TL::NW, EACH = SPAN / NW;
+  static_assert(SPAN % NW == 0, "a span's tiles are shared out to the waves");
+  auto slot = [&](int i) { return (REVERSE ? NW - 1 - i : i) * C + c; };
+  const int span = order / SPAN, start = span * SPAN;
+  word_t* states = words + (int64_t)tiles * C + c;
+  words += c;
   float P = 1.f, U = 0.f;
+  if (wave == 0 && exists && tiles > 1) {
 #pragma unroll 4
-  for (int i = 0; i < NW; ++i) {
-    const int at = (REVERSE ? NW - 1 - i : i) * C + c;
-    U = fmaf(sP[at], U, sU[at]);
-    P *= sP[at];
-  }
-  float h = first;
-  if (tiles > 1) {
-    const int span = order / SPAN;
-    word_t* states = words + (int64_t)tiles * 2 * C + c;
-    words += c;
-    if (order % SPAN != SPAN - 1 && order + 1 < tiles) {  // someone may read the tile's step
-      put_word(words + (int64_t)order * 2 * C, P);
-      put_word(words + ((int64_t)order * 2 + 1) * C, U);
+    for (int i = 0; i < NW; ++i) {
+      U = fmaf(j.P[slot(i)], U, j.U[slot(i)]);
+      P *= j.P[slot(i)];
     }
+    if (order % SPAN != SPAN - 1 && order + 1 < tiles)  // someone may read the tile's step
+      put_word(words + (int64_t)order * C, __float_as_uint(P) | MARK, U);
+  }
+  if (order > start) {
+    const int t0 = start + wave * EACH;
+    if (exists) {
+      float p = 1.f, u = 0.f;
+      if (t0 < order) {
+        word_t w[EACH];
+        bool all;
+        do {
+          all = true;
+#pragma unroll
+          for (int i = 0; i < EACH; ++i) w[i] = get_word(words + (int64_t)(t0 + i < order ? t0 + i : t0) * C);
+#pragma unroll
+          for (int i = 0; i < EACH; ++i) all = all && is_there(w[i]);
+        } while (!all);
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+          if (t0 + i < order) {
+            u = fmaf(step_p(w[i]), u, low_value(w[i]));
+            p *= step_p(w[i]);
+          }
+      }
+      j.spanP[wave * C + c] = p;
+      j.spanU[wave * C + c] = u;
+    }
+    __syncthreads();
+  }
+  if (wave == 0 && exists) {
+    float h = first;
     if (span) {
       word_t s;
       while (!is_there(s = get_word(states + (int64_t)span * C))) __builtin_amdgcn_s_sleep(1);
-      h = value_of(s);
+      h = low_value(s);
     }
-    constexpr int BATCH = 4;  // steps waited for at once
-    for (int t = span * SPAN; t < order; t += BATCH) {
-      word_t p[BATCH], u[BATCH];
-      bool all;
-      do {
-        all = true;
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-          const int64_t at = t + i < order ? t + i : t;
-          p[i] = get_word(words + at * 2 * C);
-          u[i] = get_word(words + (at * 2 + 1) * C);
-        }
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) all = all && is_there(p[i]) && is_there(u[i]);
-      } while (!all);
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i)
-        if (t + i < order) h = fmaf(value_of(p[i]), h, value_of(u[i]));
-    }
-    if (order % SPAN == SPAN - 1 && order + 1 < tiles)
-      put_word(states + ((int64_t)span + 1) * C, fmaf(P, h, U));
-  }
+    if (order > start)
 #pragma unroll 4
-  for (int i = 0; i < NW; ++i) {
-    const int at = (REVERSE ? NW - 1 - i : i) * C + c;
-    sH[at] = h;
-    h = fmaf(sP[at], h, sU[at]);
+      for (int i = 0; i < NW; ++i) h = fmaf(j.spanP[i * C + c], h, j.spanU[i * C + c]);
+    if (order % SPAN == SPAN - 1 && order + 1 < tiles)
+      put_word(states + ((int64_t)span + 1) * C, MARK, fmaf(P, h, U));
+#pragma unroll 4
+    for (int i = 0; i < NW; ++i) {
+      j.H[slot(i)] = h;
+      h = fmaf(j.P[slot(i)], h, j.U[slot(i)]);
+    }
   }
+  __syncthreads();
 }
 
 // the next tile of this workgroup's head (in the scan's order)
@@ -234,7 +271,7 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan(
     const float* __restrict__ h0, int64_t N, int DH, int slabs, int heads, int tiles,
     float* __restrict__ y, float* __restrict__ hf, unsigned* counters, word_t* words) {
   constexpr int V = TL::V, TT = TL::TT, C = TL::C;
-  __shared__ float sP[TL::NW * C], sU[TL::NW * C], sH[TL::NW * C];
+  __shared__ Joint<TL> j;
   const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
   const int hs = blockIdx.x % heads;  // head and slab
   const int tile = take_tile(tiles, counters + hs);
@@ -260,28 +297,26 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan(
   }
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
-    const bool in = sp.tok + i < sp.rows;
+    rA[i].or_else(sp.tok + i < sp.rows, 0xff80u);  // tokens past the end leave the state alone:
+    rx[i].or_else(sp.tok + i < sp.rows, 0u);       // A_P = -inf, x = 0
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      // tokens past the end leave the state alone: a = 1, x = 0
-      float rest, beta, db;
-      decay_of<SCALE>(in ? rA[i].get(v) : -INFINITY, a[i][v], rest, beta, db);
-      float g = 1.f;
+      float beta, g = 1.f;
+      decay_of<SCALE>(rA[i].get(v), a[i][v], beta);
       if constexpr (GATE) g = sigmoid_v(rI[i].get(v));
-      u[i][v] = beta * g * (in ? rx[i].get(v) : 0.f);
+      u[i][v] = beta * g * rx[i].get(v);
       U[v] = fmaf(a[i][v], U[v], u[i][v]);
       P[v] *= a[i][v];
     }
   }
-  scan_groups<TL, false>(P, U, lane, sP + wave * C, sU + wave * C);
+  scan_groups<TL, false>(P, U, lane, j.P + wave * C, j.U + wave * C);
   __syncthreads();
-  if (wave == 0 && lane < C && hs % slabs * C + lane < DH)
-    join_tiles<TL, false>(sP, sU, sH, lane, tile, tiles, h0 ? h0[sp.state + lane] : 0.f,
-                          words + hs * slab_words(tiles, C));
-  __syncthreads();
+  const bool exists = lane < C && hs % slabs * C + lane < DH;
+  join_tiles<TL, false>(j, wave, lane, exists, tile, tiles, wave == 0 && exists && h0 ? h0[sp.state + lane] : 0.f,
+                        words + hs * slab_words(tiles, C));
   float h[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = fmaf(P[v], sH[wave * C + sp.c + v], U[v]);
+  for (int v = 0; v < V; ++v) h[v] = fmaf(P[v], j.H[wave * C + sp.c + v], U[v]);
   const bool last = tile == tiles - 1 && hf;
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
@@ -307,7 +342,7 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
     float* __restrict__ dx, float* __restrict__ dA, float* __restrict__ dI,
     float* __restrict__ dh0, unsigned* counters, word_t* words) {
   constexpr int V = TL::V, TT = TL::TT, C = TL::C;
-  __shared__ float sP[TL::NW * C], sU[TL::NW * C], sH[TL::NW * C];
+  __shared__ Joint<TL> j;
   const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
   const int hs = blockIdx.x % heads;
   const int order = take_tile(tiles, counters + hs), tile = tiles - 1 - order;
@@ -345,27 +380,29 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
     U[v] = 0.f;
   }
 #pragma unroll
-  for (int i = TT - 1; i >= 0; --i)
+  for (int i = TT - 1; i >= 0; --i) {
+    rA[i].or_else(sp.tok + i < sp.rows, 0xff80u);  // tokens past the end: a = 1, dy = 0
+    rd[i].or_else(sp.tok + i < sp.rows, 0u);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const bool in = sp.tok + i < sp.rows;  // tokens past the end: a = 1, dy = 0
       float a, rest;
-      sigmoid_pair(in ? rA[i].get(v) : -INFINITY, rest, a);
-      U[v] = a * ((in ? rd[i].get(v) : 0.f) + U[v]);
+      sigmoid_pair(rA[i].get(v), rest, a);
+      U[v] = a * (rd[i].get(v) + U[v]);
       P[v] *= a;
     }
-  scan_groups<TL, true>(P, U, lane, sP + wave * C, sU + wave * C);
+  }
+  scan_groups<TL, true>(P, U, lane, j.P + wave * C, j.U + wave * C);
   __syncthreads();
-  if (wave == 0 && lane < C && hs % slabs * C + lane < DH)
-    join_tiles<TL, true>(sP, sU, sH, lane, order, tiles, dlast ? dlast[sp.state + lane] : 0.f,
-                         words + hs * slab_words(tiles, C));
-  __syncthreads();
+  const bool exists = lane < C && hs % slabs * C + lane < DH;
+  join_tiles<TL, true>(j, wave, lane, exists, order, tiles,
+                       wave == 0 && exists && dlast ? dlast[sp.state + lane] : 0.f,
+                       words + hs * slab_words(tiles, C));
   // the decays are computed again rather than held over the wait
 #pragma unroll
   for (int i = 0; i < TT; ++i) rA[i].forget();
   float carry[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) carry[v] = fmaf(P[v], sH[wave * C + sp.c + v], U[v]);
+  for (int v = 0; v < V; ++v) carry[v] = fmaf(P[v], j.H[wave * C + sp.c + v], U[v]);
 #pragma unroll
   for (int i = TT - 1; i >= 0; --i) {
     if (!sp.live || sp.tok + i >= sp.rows) continue;
@@ -373,7 +410,7 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float a, rest, beta, db, g = 1.f;
-      decay_of<SCALE>(rA[i].get(v), a, rest, beta, db);
+      decay_slope<SCALE>(rA[i].get(v), a, rest, beta, db);
       const float lam = rd[i].get(v) + carry[v], xv = rx[i].get(v);
       if constexpr (GATE) {
         float ng;
@@ -402,8 +439,8 @@ __global__ __launch_bounds__(256) void k_gated_step(const T* __restrict__ x, con
                                                     int64_t n, float* out) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
-  float a, rest, beta, db;
-  decay_of<SCALE>(Elem<T>::ld(A, i), a, rest, beta, db);
+  float a, beta;
+  decay_of<SCALE>(Elem<T>::ld(A, i), a, beta);
   const float g = I ? sigmoid_v(Elem<T>::ld(I, i)) : 1.f;
   out[i] = fmaf(a, state[i], beta * g * Elem<T>::ld(x, i));
 }

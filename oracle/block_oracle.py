@@ -49,33 +49,45 @@ def scan(x, A, I, h0, scale):
     return y
 
 
-def _path(a, v, m):
-    """For h_t = a_t h_{t-1} + v_t started from m: the sums of |terms| and of
-    |terms| times the steps that each has been carried."""
+def _path(a, step, v, term, m):
+    """For h_t = a_t h_{t-1} + v_t started from m: the sums of |terms|, and the
+    roundings they carry: `step` for each step of a term, `term` at its start."""
     q = np.zeros_like(m)
     ms, qs = np.empty(a.shape), np.empty(a.shape)
     for t in range(a.shape[-2]):
-        q = a[..., t, :] * (q + m)
-        m = a[..., t, :] * m + np.abs(v[..., t, :])
+        now = np.abs(v[..., t, :])
+        q = a[..., t, :] * (q + step[..., t, :] * m) + term[..., t, :] * now
+        m = a[..., t, :] * m + now
         ms[..., t, :], qs[..., t, :] = m, q
     return ms, qs
 
 
-# The relative error of a: the exponential 3 U (1.5 ulp), 1 + e and its
-# reciprocal 3 U, the product 1 U: 7 U for the smaller of a and 1 - a; the larger
-# has at most that (the smaller is at most as large) and a rounding of its own:
-# 8 U.  Each carried step multiplies by a and rounds once: 9 U.  A term's own
-# start: beta 8 U / 2 + 8 U / 2 + 4 U (the root's product, sum and reciprocal
-# root), g 8 U, two products 2 U: under 30 U; joining the shares of threads,
-# waves, workgroups and segments: under 50 roundings more.
-STEP, TERM = 9.0, 80.0
+def size(x):
+    """|x| as it counts in the exponential's error: beyond 104 the value is 0 or 1."""
+    return 0.0 if x is None else np.minimum(np.abs(x), 104.0)
+
+
+# The relative error of e^{-|A|} is |A| + 3 roundings: the product with log2 e is
+# off by one (and log2 e by less), which the exponent turns into |A|, and the
+# exponential itself by one ulp.  1 + e and its reciprocal: 3, the product: 1, so
+# the smaller of a and 1 - a has |A| + 7; the larger has its own rounding and at
+# most (|A| + 7) e^{-|A|} <= 7: 8.  Each carried step multiplies by a and rounds
+# once: 9, and for A > 0, where a is the smaller, A more.  A term's own start:
+# beta |A| + 7 or less (the root halves it, and adds 3), g |I| + 7, two products
+# 2: under 30 + |A| + |I|.  Joining the shares of threads, waves, workgroups and
+# spans: under 50 more.
+STEP, TERM, JOIN = 9.0, 30.0, 50.0
+
+
+def _step(A):
+    return STEP + np.maximum(size(A) * np.sign(A), 0)
 
 
 def scan_bound(x, A, I, h0, scale):
     a, _, beta, _, g = gates(A, I, scale)
     m = np.zeros(x.shape[:-2] + x.shape[-1:]) if h0 is None else np.abs(h0).astype(np.float64)
-    ms, qs = _path(a, beta * g * x, m)
-    return U * (STEP * qs + TERM * ms) + TINY
+    ms, qs = _path(a, _step(A), beta * g * x, TERM + size(A) + size(I), m)
+    return U * (qs + JOIN * ms) + TINY
 
 
 def _reverse(a, dy, dlast):
@@ -112,11 +124,13 @@ def _before(y, h0):
 def scan_backward_bound(x, A, I, h0, y, dy, dlast, scale):
     a, rest, beta, dbeta, g = gates(A, I, scale)
     after, v = _reverse(a, dy, dlast)
-    ms, qs = _path(after, v, np.zeros(x.shape[:-2] + x.shape[-1:]))
+    step = _step(A)
+    step = np.concatenate([step[..., 1:, :], step[..., :1, :]], -2)[..., ::-1, :]
+    ms, qs = _path(after, step, v, np.ones(x.shape), np.zeros(x.shape[:-2] + x.shape[-1:]))
     ms, qs = ms[..., ::-1, :], qs[..., ::-1, :]
-    # lam's own bound, and under 60 U of the factors (a 8, 1 - a 8, a^2 16, the
-    # root 16, g 8 and 1 - g 8, products and the sum)
-    lam = U * (STEP * qs + (TERM + 60) * ms)
+    # lam's own bound, and under 60 + 3 |A| + |I| of the factors (a |A| + 8, 1 - a
+    # as much, a^2 twice, the root, g and 1 - g |I| + 8 together, products, the sum)
+    lam = U * (qs + (JOIN + 60 + 3 * size(A) + size(I)) * ms)
     prev = np.abs(_before(y, h0))
     dA = lam * (dbeta * g * np.abs(x) + a * rest * prev) + TINY
     dI = None if I is None else lam * beta * np.abs(x) * g * (1 - g) + TINY
@@ -210,9 +224,10 @@ def norm_out(y, z, w, groups, gate_first, eps):
 
 def norm_out_bound(y, z, w, groups, gate_first, eps, dtype):
     o = np.abs(norm_out(y, z, w, groups, gate_first, eps))
-    # silu: 12 roundings (exponential, sum, reciprocal, products); with the gate
-    # first they enter the mean as well, twice
-    return o * (U * (0.5 * sum_roundings(y.shape[1] * y.shape[3] // groups) + 45) + rounding(dtype)) + TINY
+    # silu: 12 + |z| roundings (exponential, sum, reciprocal, products); with the
+    # gate first they enter the mean as well, twice
+    near = 45 + 3 * np.max(size(z), initial=0)
+    return o * (U * (0.5 * sum_roundings(y.shape[1] * y.shape[3] // groups) + near) + rounding(dtype)) + TINY
 
 
 def norm_out_backward(do, y, z, w, groups, gate_first, eps):
@@ -239,11 +254,12 @@ def norm_out_backward_bound(do, y, z, w, groups, gate_first, eps):
     t = np.abs(yr) * gate if gate_first else np.abs(yr)
     k, n = _inv(t, eps), sum_roundings(yr.shape[-1])
     c = do4 * w4 * (1 if gate_first else gate)
-    e = U * ((0.5 * n + 60) * k * c + (2.5 * n + 150) * k ** 3 * np.mean(c * t, -1, keepdims=True) * t)
+    far = 4 * np.max(size(z), initial=0)  # of the logistic: |z| in silu and in its slope
+    e = U * ((0.5 * n + 60 + far) * k * c + (2.5 * n + 150 + 3 * far) * k ** 3 * np.mean(c * t, -1, keepdims=True) * t)
     R = y.shape[0] * y.shape[2]
     if gate_first:
         dy, dz = e * gate, e * np.abs(yr) * slope
     else:
-        dy, dz = e, U * (0.5 * n + 60) * do4 * w4 * np.abs(yr) * k * slope
-    dw = U * (0.5 * n + 60 + R) * np.sum(do4 * t * k * (1 if gate_first else gate), (0, 1))
+        dy, dz = e, U * (0.5 * n + 60 + far) * do4 * w4 * np.abs(yr) * k * slope
+    dw = U * (0.5 * n + 60 + far + R) * np.sum(do4 * t * k * (1 if gate_first else gate), (0, 1))
     return _heads(dy, y.shape) + TINY, dz.reshape(z.shape) + TINY, dw.reshape(w.shape) + TINY

@@ -30,19 +30,40 @@ __device__ __forceinline__ float sigmoid_v(float x) {
   return __builtin_amdgcn_rcpf(1.f + exp_fast(-x));
 }
 
+// Nontemporal accesses (NT), for arrays that pass through once and are larger
+// than the last-level cache: they leave the caches to what is used again.
+template <bool NT, typename P>
+__device__ __forceinline__ P load_as(const void* p) {
+  const P* q = static_cast<const P*>(p);
+  if constexpr (NT) return __builtin_nontemporal_load(q);
+  return *q;
+}
+
+template <bool NT, typename P>
+__device__ __forceinline__ void store_as(void* p, P v) {
+  P* q = static_cast<P*>(p);
+  if constexpr (NT) {
+    __builtin_nontemporal_store(v, q);
+  } else {
+    *q = v;
+  }
+}
+
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+
 // V consecutive elements of a row as they are stored.  or_else(): the elements,
 // or one bit pattern for all of them (fp32's upper half) where `in` is false;
 // forget(): what was computed from them is not kept for later use.
 template <typename T, int V> struct Raw;
 template <> struct Raw<uint16_t, 4> {
-  uint2 r;
+  u32x2 r;
   __device__ __forceinline__ void or_else(bool in, unsigned other) {
     other = other << 16 | other;
     r.x = in ? r.x : other;
     r.y = in ? r.y : other;
   }
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r.x), "+v"(r.y)); }
-  __device__ __forceinline__ void load(const uint16_t* p) { r = *reinterpret_cast<const uint2*>(p); }
+  template <bool NT = false> __device__ __forceinline__ void load(const uint16_t* p) { r = load_as<NT, u32x2>(p); }
   __device__ __forceinline__ float get(int v) const {
     const unsigned w = v < 2 ? r.x : r.y;
     return __uint_as_float(v % 2 ? w & 0xffff0000u : w << 16);
@@ -55,40 +76,38 @@ template <> struct Raw<float, 4> {
     for (int v = 0; v < 4; ++v) r[v] = in ? r[v] : __uint_as_float(other << 16);
   }
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
-  __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const f32x4*>(p); }
+  template <bool NT = false> __device__ __forceinline__ void load(const float* p) { r = load_as<NT, f32x4>(p); }
   __device__ __forceinline__ float get(int v) const { return r[v]; }
 };
 template <> struct Raw<uint16_t, 1> {
   uint16_t r;
   __device__ __forceinline__ void or_else(bool in, unsigned other) { r = in ? r : (uint16_t)other; }
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
-  __device__ __forceinline__ void load(const uint16_t* p) { r = *p; }
+  template <bool NT = false> __device__ __forceinline__ void load(const uint16_t* p) { r = load_as<NT, uint16_t>(p); }
   __device__ __forceinline__ float get(int) const { return bf16_to_f32(r); }
 };
 template <> struct Raw<float, 1> {
   float r;
   __device__ __forceinline__ void or_else(bool in, unsigned other) { r = in ? r : __uint_as_float(other << 16); }
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
-  __device__ __forceinline__ void load(const float* p) { r = *p; }
+  template <bool NT = false> __device__ __forceinline__ void load(const float* p) { r = load_as<NT, float>(p); }
   __device__ __forceinline__ float get(int) const { return r; }
 };
 
-template <int V>
+template <int V, bool NT = false>
 __device__ __forceinline__ void store_row(float* p, const float (&v)[V]) {
   if constexpr (V == 4)
-    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    store_as<NT>(p, f32x4{v[0], v[1], v[2], v[3]});
   else
-    *p = v[0];
+    store_as<NT>(p, v[0]);
 }
 
-template <int V>
+template <int V, bool NT = false>
 __device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[V]) {
-  __bf16* q = reinterpret_cast<__bf16*>(p);
   if constexpr (V == 4)
-    *reinterpret_cast<bf16x4*>(q) =
-        bf16x4{f32_to_bf16(v[0]), f32_to_bf16(v[1]), f32_to_bf16(v[2]), f32_to_bf16(v[3])};
+    store_as<NT>(p, bf16x4{f32_to_bf16(v[0]), f32_to_bf16(v[1]), f32_to_bf16(v[2]), f32_to_bf16(v[3])});
   else
-    *q = f32_to_bf16(v[0]);
+    store_as<NT>(p, f32_to_bf16(v[0]));
 }
 
 }  // namespace ssd

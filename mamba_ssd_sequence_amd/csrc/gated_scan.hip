@@ -160,10 +160,10 @@ struct Joint {
 // From the waves' steps in LDS (complete) to the state entering each wave
 // (j.H, complete on return), by way of the other tiles; lane c < C of a wave is
 // channel c, `exists` says whether the head has it.  `order`: the tile's place
-// in the scan's direction; `first`: the state entering the whole sequence, in
-// the first wave's lanes.
+// in the scan's direction; `first`: in the first wave's lanes, the state
+// entering the whole sequence.  Returns, there, the state that leaves the tile.
 template <typename TL, bool REVERSE>
-__device__ __forceinline__ void join_tiles(Joint<TL>& j, int wave, int c, bool exists, int order,
+__device__ __forceinline__ float join_tiles(Joint<TL>& j, int wave, int c, bool exists, int order,
                                            int tiles, float first, word_t* words) {
   constexpr int C = TL::C, NW = TL::NW, EACH = SPAN / NW;
   static_assert(SPAN % NW == 0, "a span's tiles are shared out to the waves");
@@ -207,8 +207,8 @@ __device__ __forceinline__ void join_tiles(Joint<TL>& j, int wave, int c, bool e
     }
     __syncthreads();
   }
+  float h = first;
   if (wave == 0 && exists) {
-    float h = first;
     if (span) {
       word_t s;
       while (!is_there(s = get_word(states + (int64_t)span * C))) __builtin_amdgcn_s_sleep(1);
@@ -226,6 +226,7 @@ __device__ __forceinline__ void join_tiles(Joint<TL>& j, int wave, int c, bool e
     }
   }
   __syncthreads();
+  return h;
 }
 
 // the next tile of this workgroup's head (in the scan's order)
@@ -268,26 +269,30 @@ struct Spot {
 template <typename T, int SCALE, bool GATE, typename TL>
 __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan(
     const T* __restrict__ x, const T* __restrict__ A, const T* __restrict__ I,
-    const float* __restrict__ h0, int64_t N, int DH, int slabs, int heads, int tiles,
+    const float* __restrict__ h0, int64_t N, int DH, int slabs, int heads, int tiles, int runs,
     float* __restrict__ y, float* __restrict__ hf, unsigned* counters, word_t* words) {
   constexpr int V = TL::V, TT = TL::TT, C = TL::C;
   __shared__ Joint<TL> j;
   const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
   const int hs = blockIdx.x % heads;  // head and slab
-  const int tile = take_tile(tiles, counters + hs);
+  const int taken = take_tile(tiles, counters + hs);
+  const bool exists = lane < C && hs % slabs * C + lane < DH;
+  float enter = 0.f;  // in the first wave: the state entering the sequence, then each next tile
+  if (wave == 0 && exists && h0) enter = h0[(int64_t)(hs / slabs) * DH + hs % slabs * C + lane];
+  for (int k = 0; k < runs; ++k) {
+  const int tile = taken + k;
+  asm("" : "+s"(DH));  // a tile's offsets are not worth registers over the loop
   const Spot<TL> sp(hs, tile, N, DH, slabs);
-  x += sp.base;
-  A += sp.base;
-  I += sp.base;
-  y += sp.base;
+  const T *xt = x + sp.base, *At = A + sp.base, *It = I + sp.base;
+  float* yt = y + sp.base;
 
   Raw<T, V> rx[TT], rA[TT], rI[TT];
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
     const unsigned at = sp.at(i, DH);
-    rA[i].load(A + at);
-    if constexpr (GATE) rI[i].load(I + at);
-    rx[i].load(x + at);
+    rA[i].template load<true>(At + at);
+    if constexpr (GATE) rI[i].template load<true>(It + at);
+    rx[i].template load<true>(xt + at);
   }
   float a[TT][V], u[TT][V], P[V], U[V];
 #pragma unroll
@@ -311,21 +316,21 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan(
   }
   scan_groups<TL, false>(P, U, lane, j.P + wave * C, j.U + wave * C);
   __syncthreads();
-  const bool exists = lane < C && hs % slabs * C + lane < DH;
-  join_tiles<TL, false>(j, wave, lane, exists, tile, tiles, wave == 0 && exists && h0 ? h0[sp.state + lane] : 0.f,
-                        words + hs * slab_words(tiles, C));
+  enter = join_tiles<TL, false>(j, wave, lane, exists, tiles > 1 ? tile : 0, tiles, enter,
+                                words + hs * slab_words(tiles, C));
   float h[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) h[v] = fmaf(P[v], j.H[wave * C + sp.c + v], U[v]);
-  const bool last = tile == tiles - 1 && hf;
+  const bool last = tile == tiles * runs - 1 && hf;
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], u[i][v]);
     if (sp.live && sp.tok + i < sp.rows) {
-      store_row<V>(y + sp.at(i, DH), h);
+      store_row<V, true>(yt + sp.at(i, DH), h);
       if (last && sp.tok + i == sp.rows - 1) store_row<V>(hf + sp.state + sp.c, h);
     }
+  }
   }
 }
 
@@ -338,39 +343,40 @@ template <typename T, int SCALE, bool GATE, typename TL>
 __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
     const T* __restrict__ x, const T* __restrict__ A, const T* __restrict__ I,
     const float* __restrict__ h0, const float* __restrict__ y, const float* __restrict__ dy,
-    const float* __restrict__ dlast, int64_t N, int DH, int slabs, int heads, int tiles,
+    const float* __restrict__ dlast, int64_t N, int DH, int slabs, int heads, int tiles, int runs,
     float* __restrict__ dx, float* __restrict__ dA, float* __restrict__ dI,
     float* __restrict__ dh0, unsigned* counters, word_t* words) {
   constexpr int V = TL::V, TT = TL::TT, C = TL::C;
   __shared__ Joint<TL> j;
   const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
   const int hs = blockIdx.x % heads;
-  const int order = take_tile(tiles, counters + hs), tile = tiles - 1 - order;
+  const int taken = take_tile(tiles, counters + hs);
+  const bool exists = lane < C && hs % slabs * C + lane < DH;
+  float enter = 0.f;  // in the first wave: d_final_state, then the c that leaves each tile
+  if (wave == 0 && exists && dlast) enter = dlast[(int64_t)(hs / slabs) * DH + hs % slabs * C + lane];
+  for (int k = 0; k < runs; ++k) {
+  const int order = taken + k, tile = tiles * runs - 1 - order;
+  asm("" : "+s"(DH));  // a tile's offsets are not worth registers over the loop
   const Spot<TL> sp(hs, tile, N, DH, slabs);
-  x += sp.base;
-  A += sp.base;
-  I += sp.base;
-  dy += sp.base;
-  y += sp.base - DH;  // a row before the tile: the states before each token
-  dx += sp.base;
-  dA += sp.base;
-  dI += sp.base;
+  const T *xt = x + sp.base, *At = A + sp.base, *It = I + sp.base;
+  const float *dyt = dy + sp.base, *yt = y + sp.base - DH;  // yt: a row before, the states before each token
+  float *dxt = dx + sp.base, *dAt = dA + sp.base, *dIt = dI + sp.base;
   const bool first = tile == 0 && sp.tok == 0;  // the sequence's first token: the state before it is h0
 
   Raw<T, V> rA[TT], rx[TT], rI[TT];
   Raw<float, V> rd[TT], rp[TT], r0;
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
-    rA[i].load(A + sp.at(i, DH));
-    rd[i].load(dy + sp.at(i, DH));
+    rA[i].template load<true>(At + sp.at(i, DH));
+    rd[i].template load<true>(dyt + sp.at(i, DH));
   }
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
     const unsigned at = sp.at(i, DH);
-    rx[i].load(x + at);
-    if constexpr (GATE) rI[i].load(I + at);
+    rx[i].template load<true>(xt + at);
+    if constexpr (GATE) rI[i].template load<true>(It + at);
     // the row before; before the sequence's first row there is none, and its own is read without use
-    rp[i].load(y + (tile == 0 && at < (unsigned)DH ? at + DH : at));
+    rp[i].template load<true>(yt + (tile == 0 && at < (unsigned)DH ? at + DH : at));
   }
   if (tile == 0 && h0) r0.load(h0 + sp.state + sp.c);
   float P[V], U[V];
@@ -393,10 +399,8 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
   }
   scan_groups<TL, true>(P, U, lane, j.P + wave * C, j.U + wave * C);
   __syncthreads();
-  const bool exists = lane < C && hs % slabs * C + lane < DH;
-  join_tiles<TL, true>(j, wave, lane, exists, order, tiles,
-                       wave == 0 && exists && dlast ? dlast[sp.state + lane] : 0.f,
-                       words + hs * slab_words(tiles, C));
+  enter = join_tiles<TL, true>(j, wave, lane, exists, tiles > 1 ? order : 0, tiles, enter,
+                               words + hs * slab_words(tiles, C));
   // the decays are computed again rather than held over the wait
 #pragma unroll
   for (int i = 0; i < TT; ++i) rA[i].forget();
@@ -424,10 +428,11 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
       carry[v] = a * lam;
     }
     const unsigned at = sp.at(i, DH);
-    store_row<V>(dx + at, ox);
-    store_row<V>(dA + at, oA);
-    if constexpr (GATE) store_row<V>(dI + at, oI);
+    store_row<V, true>(dxt + at, ox);
+    store_row<V, true>(dAt + at, oA);
+    if constexpr (GATE) store_row<V, true>(dIt + at, oI);
     if (i == 0 && first && dh0) store_row<V>(dh0 + sp.state + sp.c, carry);
+  }
   }
 }
 
@@ -466,33 +471,47 @@ static int tile_kind(int64_t DH) { return DH % 4 ? NARROW : DH > 32 ? WIDE64 : W
 constexpr int kind_lpr(int k) { return k == WIDE32 ? 8 : 16; }
 constexpr int kind_v(int k) { return k == NARROW ? 1 : 4; }
 
-constexpr int FWD_WAVES = 8, BWD_WAVES = 8;
+// Tokens a thread: what its registers hold (16 waves of 128 a CU).
 constexpr int fwd_tokens(bool bf16) { return bf16 ? 8 : 4; }
 constexpr int BWD_TOKENS = 4;
 
+// How a call is cut.  A workgroup of 16 waves has the larger tile, so fewer
+// steps to publish and wait for, but a CU holds only one; two of 8 waves take
+// turns at loading and storing.  16 waves where there are at most 512 of their
+// tiles (4 heads x 16 of 2048 tokens, bf16: 18.8 us against 21.0; backwards 45.7
+// against 51.0), 8 beyond (8192 tokens: 65.8 against 72.3).  With 512 heads and
+// slabs or more the chip is full without cutting sequences: a workgroup runs
+// its head's tiles one after the other and nothing is published (32 x 16 heads
+// of 2048 tokens: 121 us against 125).
 struct Split {
-  int64_t slabs, heads, tiles;
-  int C;
+  int64_t slabs, heads, tiles;  // tiles: those that workgroups of one head share out
+  int waves, runs, C;           // runs: tiles that a workgroup takes one after the other (then tiles = 1)
   // floats: the counters, padded, then the words
   size_t counters() const { return (size_t)((heads + 63) & ~(int64_t)63); }
   size_t floats() const { return tiles > 1 ? counters() + (size_t)(heads * slab_words(tiles, C)) * 2 : 0; }
 };
 
-static Split split_of(int64_t BH, int64_t N, int64_t DH, int waves, int tokens) {
+static Split split_of(int64_t BH, int64_t N, int64_t DH, int tokens) {
   const int k = tile_kind(DH), lpr = kind_lpr(k), C = lpr * kind_v(k);
-  const int64_t slabs = (DH + C - 1) / C, per = (int64_t)waves * (WAVE / lpr) * tokens;
-  return {slabs, BH * slabs, (N + per - 1) / per, C};
+  const int64_t slabs = (DH + C - 1) / C, heads = BH * slabs;
+  auto tiles = [&](int waves) {
+    const int64_t per = (int64_t)waves * (WAVE / lpr) * tokens;
+    return (N + per - 1) / per;
+  };
+  if (heads * tiles(16) <= 512) return {slabs, heads, tiles(16), 16, 1, C};
+  if (heads >= 512) return {slabs, heads, 1, 8, (int)tiles(8), C};
+  return {slabs, heads, tiles(8), 8, 1, C};
 }
 
 // for either element type
 size_t gated_scan_floats(int64_t BH, int64_t N, int64_t DH) {
-  const size_t a = split_of(BH, N, DH, FWD_WAVES, fwd_tokens(true)).floats();
-  const size_t b = split_of(BH, N, DH, FWD_WAVES, fwd_tokens(false)).floats();
+  const size_t a = split_of(BH, N, DH, fwd_tokens(true)).floats();
+  const size_t b = split_of(BH, N, DH, fwd_tokens(false)).floats();
   return a > b ? a : b;
 }
 
 size_t gated_scan_backward_floats(int64_t BH, int64_t N, int64_t DH) {
-  return split_of(BH, N, DH, BWD_WAVES, BWD_TOKENS).floats();
+  return split_of(BH, N, DH, BWD_TOKENS).floats();
 }
 
 static hipError_t clear_words(const Split& s, float* ws, hipStream_t stream) {
@@ -503,33 +522,37 @@ static hipError_t clear_words(const Split& s, float* ws, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// calls f(T, SCALE, GATE, kind) with types for the call's element type, scale, gate and tile
+// calls f(T, SCALE, GATE, kind, NW) with types for the call's element type, scale, gate, tile and waves
 template <typename F>
-static hipError_t by_call(bool bf16, int scale, bool gate, int64_t DH, F&& f) {
+static hipError_t by_call(bool bf16, int scale, bool gate, int64_t DH, int waves, F&& f) {
   return by_type(bf16, scale, [&](auto t, auto sc) {
-    auto with = [&](auto g) {
+    auto with = [&](auto g, auto k) {
+      return waves == 16 ? f(t, sc, g, k, std::integral_constant<int, 16>{})
+                         : f(t, sc, g, k, std::integral_constant<int, 8>{});
+    };
+    auto by_kind = [&](auto g) {
       switch (tile_kind(DH)) {
-        case WIDE64: return f(t, sc, g, std::integral_constant<int, WIDE64>{});
-        case WIDE32: return f(t, sc, g, std::integral_constant<int, WIDE32>{});
-        default: return f(t, sc, g, std::integral_constant<int, NARROW>{});
+        case WIDE64: return with(g, std::integral_constant<int, WIDE64>{});
+        case WIDE32: return with(g, std::integral_constant<int, WIDE32>{});
+        default: return with(g, std::integral_constant<int, NARROW>{});
       }
     };
-    return gate ? with(std::true_type{}) : with(std::false_type{});
+    return gate ? by_kind(std::true_type{}) : by_kind(std::false_type{});
   });
 }
 
 hipError_t launch_gated_scan(bool bf16, int scale, const void* x, const void* A, const void* I,
                              const float* h0, int64_t BH, int64_t N, int64_t DH, float* y,
                              float* hf, float* ws, hipStream_t stream) {
-  const Split s = split_of(BH, N, DH, FWD_WAVES, fwd_tokens(bf16));
+  const Split s = split_of(BH, N, DH, fwd_tokens(bf16));
   const hipError_t e = clear_words(s, ws, stream);
   if (e != hipSuccess) return e;
-  return by_call(bf16, scale, I != nullptr, DH, [&](auto t, auto sc, auto g, auto k) {
+  return by_call(bf16, scale, I != nullptr, DH, s.waves, [&](auto t, auto sc, auto g, auto k, auto nw) {
     using T = decltype(t);
-    using TL = Tile<kind_v(k.value), kind_lpr(k.value), FWD_WAVES, fwd_tokens(sizeof(T) == 2)>;
+    using TL = Tile<kind_v(k.value), kind_lpr(k.value), nw.value, fwd_tokens(sizeof(T) == 2)>;
     hipLaunchKernelGGL((k_gated_scan<T, sc.value, g.value, TL>), dim3((unsigned)(s.heads * s.tiles)),
                        dim3(TL::NW * WAVE), 0, stream, (const T*)x, (const T*)A, (const T*)I, h0, N,
-                       (int)DH, (int)s.slabs, (int)s.heads, (int)s.tiles, y, hf, (unsigned*)ws,
+                       (int)DH, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs, y, hf, (unsigned*)ws,
                        (word_t*)(ws + s.counters()));
     return hipGetLastError();
   });
@@ -551,15 +574,15 @@ hipError_t launch_gated_scan_backward(bool bf16, int scale, const void* x, const
                                       const float* dy, const float* dlast, int64_t BH, int64_t N,
                                       int64_t DH, float* dx, float* dA, float* dI, float* dh0,
                                       float* ws, hipStream_t stream) {
-  const Split s = split_of(BH, N, DH, BWD_WAVES, BWD_TOKENS);
+  const Split s = split_of(BH, N, DH, BWD_TOKENS);
   const hipError_t e = clear_words(s, ws, stream);
   if (e != hipSuccess) return e;
-  return by_call(bf16, scale, I != nullptr, DH, [&](auto t, auto sc, auto g, auto k) {
+  return by_call(bf16, scale, I != nullptr, DH, s.waves, [&](auto t, auto sc, auto g, auto k, auto nw) {
     using T = decltype(t);
-    using TL = Tile<kind_v(k.value), kind_lpr(k.value), BWD_WAVES, BWD_TOKENS>;
+    using TL = Tile<kind_v(k.value), kind_lpr(k.value), nw.value, BWD_TOKENS>;
     hipLaunchKernelGGL((k_gated_scan_bwd<T, sc.value, g.value, TL>), dim3((unsigned)(s.heads * s.tiles)),
                        dim3(TL::NW * WAVE), 0, stream, (const T*)x, (const T*)A, (const T*)I, h0, y, dy,
-                       dlast, N, (int)DH, (int)s.slabs, (int)s.heads, (int)s.tiles, dx, dA, dI, dh0,
+                       dlast, N, (int)DH, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs, dx, dA, dI, dh0,
                        (unsigned*)ws, (word_t*)(ws + s.counters()));
     return hipGetLastError();
   });

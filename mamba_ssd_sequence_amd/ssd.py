@@ -27,6 +27,7 @@ The gated linear recurrence, and the norms, gate and residual scale around a mix
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -467,42 +468,69 @@ def prep_amask_backward(A_proj, dt_proj, da, ddt=None):
 
 
 # ---- the gated linear recurrence and the norms around a mixer block ----
+#
+# The shortest of these calls take a few microseconds on the GPU, so what a call
+# costs on the host counts: tensors are checked by one condition each (the
+# message is made only when it fails), and the stream is taken as a number.
 
 
-def _gpu(named, dtypes, device, shapes):
-    """Checks of a call's tensors: (name, tensor or None) pairs on one device,
-    contiguous, of the given types and shapes."""
-    for (name, t), dtype, shape in zip(named, dtypes, shapes):
-        if t is not None:
-            _require(t, name, dtype, device)
-            if t.shape != shape:
-                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _refuse(t, name, dtype, shape, device):
+    """Why a tensor was refused."""
+    _require(t, name, dtype, device)
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _call(fn, device, *args):
+def _at(t, name, dtype, shape, index, device):
+    """The address of a call's tensor after its checks (None for None)."""
+    if t is None:
+        return None
+    try:
+        if t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, device)
+
+
+def _first(t, name):
+    """The checks of the tensor that sets a call's sizes; returns its element type and device."""
+    _require(t, name)
+    return _qkv_dtype(t), t.device
+
+
+def _raw_stream(index):
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _call(fn, index, *args):
     """fn(*args, stream) on the arrays' device and its current stream (the
     library launches on the current device)."""
     torch = _torch()
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(device)))
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(device)))
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status != SSD_OK:
+        _check(status)
+
+
+@functools.lru_cache(maxsize=256)
+def _scratch_size(name, *sizes):
+    return int(getattr(lib(), name)(*sizes))
 
 
 def _scratch(workspace, need, device):
-    """(pointer, bytes, tensor) of a call's workspace; one is allocated when None is given."""
+    """A call's workspace: (address, bytes, tensor); one is allocated when None is given."""
     if workspace is None:
         if not need:
             return None, 0, None
         workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
-    else:
-        _require(workspace, "workspace", None, device)
+        return workspace.data_ptr(), need, workspace
+    _require(workspace, "workspace", None, device)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 def gated_scan(x, A_proj, I_proj=None, *, scale: int, initial_state=None, final_state=None, y=None,
@@ -511,18 +539,17 @@ def gated_scan(x, A_proj, I_proj=None, *, scale: int, initial_state=None, final_
     (or 1) and beta by scale (SSD_INPUT_PLAIN, _CONVEX, _UNIT).  x, A_proj, I_proj [B,H,N,d_h] bf16 or
     fp32, states [B,H,d_h] fp32 (final_state is written when given); returns y [B,H,N,d_h] fp32."""
     torch = _torch()
-    _require(x, "x")
-    dev, shape, f32 = x.device, x.shape, torch.float32
-    dtype = _qkv_dtype(x)
+    kind, dev = _first(x, "x")
+    i, f32, xt, shape = dev.index, torch.float32, x.dtype, x.shape
     B, H, N, d_h = shape
+    state = (B, H, d_h)
     if y is None:
         y = torch.empty(shape, dtype=f32, device=dev)
-    _gpu((("A_proj", A_proj), ("I_proj", I_proj), ("initial_state", initial_state),
-          ("final_state", final_state), ("y", y)), (x.dtype, x.dtype, f32, f32, f32), dev,
-         (shape, shape, (B, H, d_h), (B, H, d_h), shape))
-    ws, wbytes, keep = _scratch(workspace, lib().ssd_gated_scan_workspace_size(B, H, N, d_h), dev)
-    _call(lib().ssd_gated_scan, dev, _addr(x), _addr(A_proj), _addr(I_proj), _addr(initial_state), B, H, N, d_h,
-          scale, dtype, _addr(y), _addr(final_state), ws, wbytes)
+    ws, nbytes, keep = _scratch(workspace, _scratch_size("ssd_gated_scan_workspace_size", B, H, N, d_h), dev)
+    _call(lib().ssd_gated_scan, i, x.data_ptr(), _at(A_proj, "A_proj", xt, shape, i, dev),
+          _at(I_proj, "I_proj", xt, shape, i, dev), _at(initial_state, "initial_state", f32, state, i, dev),
+          B, H, N, d_h, scale, kind, _at(y, "y", f32, shape, i, dev),
+          _at(final_state, "final_state", f32, state, i, dev), ws, nbytes)
     return y
 
 
@@ -530,17 +557,14 @@ def gated_scan_step(x, A_proj, I_proj, state, *, scale: int, new_state=None):
     """ssd_gated_scan_step: one token of S sequences, x, A_proj, I_proj (or None) [S,H,d_h], state
     [S,H,d_h] fp32.  The state is updated in place unless new_state is given; returns the new state,
     which is the step's output."""
-    torch = _torch()
-    _require(x, "x")
-    dev, shape, f32 = x.device, x.shape, torch.float32
-    dtype = _qkv_dtype(x)
+    kind, dev = _first(x, "x")
+    i, f32, xt, shape = dev.index, _torch().float32, x.dtype, x.shape
     S, H, d_h = shape
     if new_state is None:
         new_state = state
-    _gpu((("A_proj", A_proj), ("I_proj", I_proj), ("state", state), ("new_state", new_state)),
-         (x.dtype, x.dtype, f32, f32), dev, (shape, shape, shape, shape))
-    _call(lib().ssd_gated_scan_step, dev, _addr(x), _addr(A_proj), _addr(I_proj), _addr(state), S, H, d_h, scale,
-          dtype, _addr(new_state))
+    _call(lib().ssd_gated_scan_step, i, x.data_ptr(), _at(A_proj, "A_proj", xt, shape, i, dev),
+          _at(I_proj, "I_proj", xt, shape, i, dev), _at(state, "state", f32, shape, i, dev), S, H, d_h, scale, kind,
+          _at(new_state, "new_state", f32, shape, i, dev))
     return new_state
 
 
@@ -550,20 +574,21 @@ def gated_scan_backward(x, A_proj, I_proj, y, dy, *, scale: int, initial_state=N
     (None without initial_state), all fp32.  y: gated_scan's output; dy, d_final_state (or None): the
     gradients with respect to y and the final state."""
     torch = _torch()
-    _require(x, "x")
-    dev, shape, f32 = x.device, x.shape, torch.float32
-    dtype = _qkv_dtype(x)
+    kind, dev = _first(x, "x")
+    i, f32, xt, shape = dev.index, torch.float32, x.dtype, x.shape
     B, H, N, d_h = shape
-    _gpu((("A_proj", A_proj), ("I_proj", I_proj), ("y", y), ("dy", dy), ("initial_state", initial_state),
-          ("d_final_state", d_final_state)), (x.dtype, x.dtype, f32, f32, f32, f32), dev,
-         (shape, shape, shape, shape, (B, H, d_h), (B, H, d_h)))
-    dx, dA = torch.empty_like(y), torch.empty_like(y)
-    dI = torch.empty_like(y) if I_proj is not None else None
-    dh0 = torch.empty_like(initial_state) if initial_state is not None else None
-    ws, wbytes, keep = _scratch(workspace, lib().ssd_gated_scan_backward_workspace_size(B, H, N, d_h), dev)
-    _call(lib().ssd_gated_scan_backward, dev, _addr(x), _addr(A_proj), _addr(I_proj), _addr(initial_state),
-          _addr(y), _addr(dy), _addr(d_final_state), B, H, N, d_h, scale, dtype, _addr(dx), _addr(dA), _addr(dI),
-          _addr(dh0), ws, wbytes)
+    state = (B, H, d_h)
+    dx = torch.empty(shape, dtype=f32, device=dev)
+    dA = torch.empty(shape, dtype=f32, device=dev)
+    dI = torch.empty(shape, dtype=f32, device=dev) if I_proj is not None else None
+    dh0 = torch.empty(state, dtype=f32, device=dev) if initial_state is not None else None
+    ws, nbytes, keep = _scratch(workspace, _scratch_size("ssd_gated_scan_backward_workspace_size", B, H, N, d_h), dev)
+    _call(lib().ssd_gated_scan_backward, i, x.data_ptr(), _at(A_proj, "A_proj", xt, shape, i, dev),
+          _at(I_proj, "I_proj", xt, shape, i, dev), _at(initial_state, "initial_state", f32, state, i, dev),
+          _at(y, "y", f32, shape, i, dev), _at(dy, "dy", f32, shape, i, dev),
+          _at(d_final_state, "d_final_state", f32, state, i, dev), B, H, N, d_h, scale, kind, dx.data_ptr(),
+          dA.data_ptr(), dI.data_ptr() if dI is not None else None, dh0.data_ptr() if dh0 is not None else None,
+          ws, nbytes)
     return dx, dA, dI, dh0
 
 
@@ -575,19 +600,18 @@ def norm_in(residual, branch, branch_scale, weight, eps: float, *, dtype=None, r
     f32 = torch.float32
     _require(residual, "residual", f32)
     dev, shape = residual.device, residual.shape
-    E = shape[-1]
+    i, E = dev.index, shape[-1]
     if branch is not None:
         dtype = branch.dtype
         if residual_out is None:
-            residual_out = torch.empty_like(residual)
+            residual_out = torch.empty(shape, dtype=f32, device=dev)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=dev)
-    kind = _qkv_dtype(out)
-    _gpu((("branch", branch), ("branch_scale", branch_scale), ("weight", weight), ("residual_out", residual_out),
-          ("out", out)), (out.dtype, f32, f32, f32, dtype), dev, (shape, (E,), (E,), shape, shape))
+    kind, dtype = _qkv_dtype(out), (out.dtype if dtype is None else dtype)
     rows = residual.numel() // E if E else 0
-    _call(lib().ssd_norm_in, dev, _addr(residual), _addr(branch), _addr(branch_scale), _addr(weight), rows, E, eps,
-          kind, _addr(residual_out), _addr(out))
+    _call(lib().ssd_norm_in, i, residual.data_ptr(), _at(branch, "branch", dtype, shape, i, dev),
+          _at(branch_scale, "branch_scale", f32, (E,), i, dev), _at(weight, "weight", f32, (E,), i, dev), rows, E,
+          eps, kind, _at(residual_out, "residual_out", f32, shape, i, dev), _at(out, "out", dtype, shape, i, dev))
     return (residual if branch is None else residual_out), out
 
 
@@ -598,26 +622,25 @@ def norm_in_backward(d_out, d_residual_out, residual_out, branch, branch_scale, 
     is then not read.  d_residual_out: fp32, or None (zero); residual_out: the r' of norm_in."""
     torch = _torch()
     f32 = torch.float32
-    _require(d_out, "d_out")
-    dev, shape = d_out.device, d_out.shape
-    kind = _qkv_dtype(d_out)
-    E = shape[-1]
+    kind, dev = _first(d_out, "d_out")
+    shape = d_out.shape
+    i, E = dev.index, shape[-1]
     if branch_scale is not None and branch is None:
         raise ValueError("branch_scale without branch")
     if branch_scale is None:
         branch = None
-    _gpu((("d_residual_out", d_residual_out), ("residual_out", residual_out), ("branch", branch),
-          ("branch_scale", branch_scale), ("weight", weight)), (f32, f32, d_out.dtype, f32, f32), dev,
-         (shape, shape, shape, (E,), (E,)))
     rows = d_out.numel() // E if E else 0
-    d_residual = torch.empty_like(residual_out)
-    d_weight = torch.empty_like(weight)
-    d_branch = torch.empty_like(residual_out) if branch is not None else None
-    d_scale = torch.empty_like(weight) if branch is not None else None
-    ws, wbytes, keep = _scratch(workspace, lib().ssd_norm_in_backward_workspace_size(rows, E), dev)
-    _call(lib().ssd_norm_in_backward, dev, _addr(d_out), _addr(d_residual_out), _addr(residual_out), _addr(branch),
-          _addr(branch_scale), _addr(weight), rows, E, eps, kind, _addr(d_residual), _addr(d_branch),
-          _addr(d_weight), _addr(d_scale), ws, wbytes)
+    d_residual = torch.empty(shape, dtype=f32, device=dev)
+    d_weight = torch.empty((E,), dtype=f32, device=dev)
+    d_branch = torch.empty(shape, dtype=f32, device=dev) if branch is not None else None
+    d_scale = torch.empty((E,), dtype=f32, device=dev) if branch is not None else None
+    ws, nbytes, keep = _scratch(workspace, _scratch_size("ssd_norm_in_backward_workspace_size", rows, E), dev)
+    _call(lib().ssd_norm_in_backward, i, d_out.data_ptr(),
+          _at(d_residual_out, "d_residual_out", f32, shape, i, dev), _at(residual_out, "residual_out", f32, shape, i, dev),
+          _at(branch, "branch", d_out.dtype, shape, i, dev), _at(branch_scale, "branch_scale", f32, (E,), i, dev),
+          _at(weight, "weight", f32, (E,), i, dev), rows, E, eps, kind, d_residual.data_ptr(),
+          d_branch.data_ptr() if branch is not None else None, d_weight.data_ptr(),
+          d_scale.data_ptr() if branch is not None else None, ws, nbytes)
     return d_residual, (d_residual if d_branch is None else d_branch), d_weight, d_scale
 
 
@@ -625,18 +648,16 @@ def norm_out(y, z, weight, eps: float, *, groups: int = 1, gate_first: bool = Tr
     """ssd_norm_out: the mixer's y [B,H,N,d_h] fp32, gated by silu(z) and normalised over `groups` groups of a
     token's channels, in token order: z and the result [B,N,H d_h] bf16 or fp32, weight [H d_h] fp32."""
     torch = _torch()
-    f32 = torch.float32
-    _require(y, "y", f32)
-    _require(z, "z", None, y.device)
-    dev = y.device
+    kind, dev = _first(z, "z")
+    i, zt = dev.index, z.dtype
+    _require(y, "y", torch.float32, dev)
     B, H, N, d_h = y.shape
     shape = (B, N, H * d_h)
-    kind = _qkv_dtype(z)
     if out is None:
-        out = torch.empty(shape, dtype=z.dtype, device=dev)
-    _gpu((("z", z), ("weight", weight), ("out", out)), (z.dtype, f32, z.dtype), dev, (shape, (H * d_h,), shape))
-    _call(lib().ssd_norm_out, dev, _addr(y), _addr(z), _addr(weight), B, H, N, d_h, groups, 1 if gate_first else 0,
-          eps, kind, _addr(out))
+        out = torch.empty(shape, dtype=zt, device=dev)
+    _call(lib().ssd_norm_out, i, y.data_ptr(), _at(z, "z", zt, shape, i, dev),
+          _at(weight, "weight", torch.float32, (H * d_h,), i, dev), B, H, N, d_h, groups, 1 if gate_first else 0, eps,
+          kind, _at(out, "out", zt, shape, i, dev))
     return out
 
 
@@ -645,17 +666,17 @@ def norm_out_backward(d_out, y, z, weight, eps: float, *, groups: int = 1, gate_
     """ssd_norm_out_backward: returns dy [B,H,N,d_h], dz [B,N,H d_h], d_weight [H d_h], all fp32."""
     torch = _torch()
     f32 = torch.float32
-    _require(y, "y", f32)
-    _require(z, "z", None, y.device)
-    dev = y.device
+    kind, dev = _first(z, "z")
+    i, zt = dev.index, z.dtype
+    _require(y, "y", f32, dev)
     B, H, N, d_h = y.shape
     shape = (B, N, H * d_h)
-    kind = _qkv_dtype(z)
-    _gpu((("d_out", d_out), ("z", z), ("weight", weight)), (z.dtype, z.dtype, f32), dev,
-         (shape, shape, (H * d_h,)))
-    dy, d_weight = torch.empty_like(y), torch.empty_like(weight)
+    dy = torch.empty(y.shape, dtype=f32, device=dev)
     dz = torch.empty(shape, dtype=f32, device=dev)
-    ws, wbytes, keep = _scratch(workspace, lib().ssd_norm_out_backward_workspace_size(B, H, N, d_h, groups), dev)
-    _call(lib().ssd_norm_out_backward, dev, _addr(d_out), _addr(y), _addr(z), _addr(weight), B, H, N, d_h, groups,
-          1 if gate_first else 0, eps, kind, _addr(dy), _addr(dz), _addr(d_weight), ws, wbytes)
+    d_weight = torch.empty((H * d_h,), dtype=f32, device=dev)
+    ws, nbytes, keep = _scratch(workspace,
+                                _scratch_size("ssd_norm_out_backward_workspace_size", B, H, N, d_h, groups), dev)
+    _call(lib().ssd_norm_out_backward, i, _at(d_out, "d_out", zt, shape, i, dev), y.data_ptr(),
+          _at(z, "z", zt, shape, i, dev), _at(weight, "weight", f32, (H * d_h,), i, dev), B, H, N, d_h, groups,
+          1 if gate_first else 0, eps, kind, dy.data_ptr(), dz.data_ptr(), d_weight.data_ptr(), ws, nbytes)
     return dy, dz, d_weight

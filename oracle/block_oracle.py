@@ -42,9 +42,10 @@ def scan(x, A, I, h0, scale):
     """h [..,N,C], a token after the other"""
     a, _, beta, _, g = gates(A, I, scale)
     h = np.zeros(x.shape[:-2] + x.shape[-1:]) if h0 is None else h0.astype(np.float64)
+    u = beta * g * x
     y = np.empty(x.shape)
     for t in range(x.shape[-2]):
-        h = a[..., t, :] * h + (beta * g * x)[..., t, :]
+        h = a[..., t, :] * h + u[..., t, :]
         y[..., t, :] = h
     return y
 

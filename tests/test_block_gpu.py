@@ -140,6 +140,13 @@ SCAN = [
     (1, 1, 4100, 200, "bf16", True, True, False),
     (40, 16, 70, 64, "bf16", True, True, True),
     (1, 1, 9000, 64, "f32", True, True, False),
+    # many tiles a head, shared out: spans of them, in workgroups of 8 and of 16 waves
+    (1, 1, 40000, 3, "bf16", True, True, False),
+    (1, 14, 20000, 32, "bf16", False, True, True),
+    (1, 12, 12000, 64, "f32", True, True, False),
+    # heads enough to take a head's tiles one after the other
+    (65, 8, 600, 64, "bf16", True, True, True),
+    (65, 8, 300, 17, "f32", False, True, False),
 ]
 
 

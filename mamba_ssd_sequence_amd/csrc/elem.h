@@ -4,6 +4,8 @@
 
 #include "common.h"
 
+#include <type_traits>
+
 namespace ssd {
 
 // e^x to (|x| + 3) roundings: 2^(x log2 e) on the hardware exponential (1 ulp),
@@ -48,6 +50,22 @@ __device__ __forceinline__ void store_as(void* p, P v) {
     *q = v;
   }
 }
+
+// f(true_type) or f(false_type): two copies of a group of accesses, kept from
+// being merged (which would drop the nontemporal ones' mark) by the empty asm
+template <typename F>
+__device__ __forceinline__ void either(bool c, F&& f) {
+  if (c) {
+    asm volatile("");
+    f(std::true_type{});
+    asm volatile("");
+  } else {
+    f(std::false_type{});
+  }
+}
+
+// The last-level cache.
+constexpr int64_t CACHE_BYTES = (int64_t)256 << 20;
 
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 

@@ -35,6 +35,7 @@ struct Geo {
   int64_t tokens;
   int groups, EG;  // groups of a token, channels of a group
   int gpw, tpw, blocks, parts;
+  bool nt_in, nt_out;  // nontemporal loads, stores
 };
 
 // A thread's place: its row's group and token, its channels.
@@ -108,12 +109,14 @@ __global__ __launch_bounds__(R::NT) void k_norm_in(const float* __restrict__ r, 
     const int64_t at = (live ? row : q.tokens - 1) * q.EG;
     Raw<float, V> rr[NV];
     Raw<T, V> rp[NV];
+    either(q.nt_in, [&](auto nt) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int e = seat.channel(k) < q.EG ? seat.channel(k) : 0;
-      rr[k].load(r + at + e);
-      if (p) rp[k].load(p + at + e);
-    }
+      for (int k = 0; k < NV; ++k) {
+        const int e = seat.channel(k) < q.EG ? seat.channel(k) : 0;
+        rr[k].template load<nt.value>(r + at + e);
+        if (p) rp[k].template load<nt.value>(p + at + e);
+      }
+    });
     float x[NV][V], sum = 0.f, none = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -125,7 +128,8 @@ __global__ __launch_bounds__(R::NT) void k_norm_in(const float* __restrict__ r, 
         x[k][v] = y;
         sum = in ? fmaf(y, y, sum) : sum;
       }
-      if (p && live && in) store_row<V>(r_out + at + seat.channel(k), x[k]);
+      if (p && live && in)
+        either(q.nt_out, [&](auto nt) { store_row<V, nt.value>(r_out + at + seat.channel(k), x[k]); });
     }
     row_sums<R>(sum, none, turn);
     const float inv = inv_rms(sum, inv_n, eps);
@@ -133,7 +137,8 @@ __global__ __launch_bounds__(R::NT) void k_norm_in(const float* __restrict__ r, 
     for (int k = 0; k < NV; ++k) {
 #pragma unroll
       for (int v = 0; v < V; ++v) x[k][v] = x[k][v] * inv * rw[k].get(v);
-      if (live && seat.channel(k) < q.EG) store_row<V>(u + at + seat.channel(k), x[k]);
+      if (live && seat.channel(k) < q.EG)
+        either(q.nt_out, [&](auto nt) { store_row<V, nt.value>(u + at + seat.channel(k), x[k]); });
     }
   }
 }
@@ -194,14 +199,16 @@ __global__ __launch_bounds__(R::NT) void k_norm_in_bwd(
     const int64_t at = (live ? row : q.tokens - 1) * q.EG;
     Raw<float, V> rr[NV], ro[NV];
     Raw<T, V> rp[NV], rd[NV];
+    either(q.nt_in, [&](auto nt) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int e = seat.channel(k) < q.EG ? seat.channel(k) : 0;
-      rr[k].load(r + at + e);
-      rd[k].load(du + at + e);
-      if (dr_out) ro[k].load(dr_out + at + e);
-      if (s) rp[k].load(p + at + e);
-    }
+      for (int k = 0; k < NV; ++k) {
+        const int e = seat.channel(k) < q.EG ? seat.channel(k) : 0;
+        rr[k].template load<nt.value>(r + at + e);
+        rd[k].template load<nt.value>(du + at + e);
+        if (dr_out) ro[k].template load<nt.value>(dr_out + at + e);
+        if (s) rp[k].template load<nt.value>(p + at + e);
+      }
+    });
     float sq = 0.f, cr = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -231,8 +238,10 @@ __global__ __launch_bounds__(R::NT) void k_norm_in_bwd(
         }
       }
       if (in) {
-        store_row<V>(dr + at + seat.channel(k), g);
-        if (s) store_row<V>(dp + at + seat.channel(k), h);
+        either(q.nt_out, [&](auto nt) {
+          store_row<V, nt.value>(dr + at + seat.channel(k), g);
+          if (s) store_row<V, nt.value>(dp + at + seat.channel(k), h);
+        });
       }
     }
   }
@@ -240,22 +249,22 @@ __global__ __launch_bounds__(R::NT) void k_norm_in_bwd(
   if (s) store_part<R>(seat, q, ds, part + (int64_t)(q.parts + seat.part) * q.EG);
 }
 
-// out[i][e] = sum over n partial rows of set i, e < E: a workgroup takes 64
-// columns, its 16 row slices of lanes add every 16th row, then each other.
+// out[i][e] = sum over n partial rows of set i, e < E: a workgroup takes 32
+// columns, its 32 row slices of lanes add every 32nd row, then each other.
 __global__ __launch_bounds__(1024) void k_sum_parts(const float* __restrict__ part, int n, int64_t E,
                                                     float* __restrict__ out0, float* __restrict__ out1) {
-  __shared__ float sums[16][64];
-  const int64_t e = (int64_t)blockIdx.x * 64 + threadIdx.x % 64;
-  const int slice = threadIdx.x / 64;
+  __shared__ float sums[32][32];
+  const int64_t e = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;
+  const int slice = threadIdx.x / 32;
   const float* src = part + (int64_t)blockIdx.y * n * E + (e < E ? e : 0);
   float sum = 0.f;
 #pragma unroll 8
-  for (int i = slice; i < n; i += 16) sum += src[i * E];
-  sums[slice][threadIdx.x % 64] = sum;
+  for (int i = slice; i < n; i += 32) sum += src[i * E];
+  sums[slice][threadIdx.x % 32] = sum;
   __syncthreads();
   if (slice || e >= E) return;
 #pragma unroll
-  for (int i = 1; i < 16; ++i) sum += sums[i][threadIdx.x];
+  for (int i = 1; i < 32; ++i) sum += sums[i][threadIdx.x];
   (blockIdx.y ? out1 : out0)[e] = sum;
 }
 
@@ -298,11 +307,13 @@ __global__ __launch_bounds__(R::NT) void k_norm_out(const float* __restrict__ y,
     const int64_t base = hd.base(token), at = token * E + e0;
     Raw<float, V> ry[NV];
     Raw<T, V> rz[NV];
+    either(q.nt_in, [&](auto nt) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      rz[k].load(z + at + (seat.channel(k) < q.EG ? seat.channel(k) : 0));
-      ry[k].load(y + base + off[k]);
-    }
+      for (int k = 0; k < NV; ++k) {
+        rz[k].template load<nt.value>(z + at + (seat.channel(k) < q.EG ? seat.channel(k) : 0));
+        ry[k].template load<nt.value>(y + base + off[k]);
+      }
+    });
     float x[NV][V], sum = 0.f, none = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -321,7 +332,8 @@ __global__ __launch_bounds__(R::NT) void k_norm_out(const float* __restrict__ y,
     for (int k = 0; k < NV; ++k) {
 #pragma unroll
       for (int v = 0; v < V; ++v) x[k][v] = x[k][v] * inv * rw[k].get(v);
-      if (live && seat.channel(k) < q.EG) store_row<V>(o + at + seat.channel(k), x[k]);
+      if (live && seat.channel(k) < q.EG)
+        either(q.nt_out, [&](auto nt) { store_row<V, nt.value>(o + at + seat.channel(k), x[k]); });
     }
   }
 }
@@ -354,13 +366,15 @@ __global__ __launch_bounds__(R::NT) void k_norm_out_bwd(
     const int64_t base = hd.base(token), at = token * E + e0;
     Raw<float, V> ry[NV];
     Raw<T, V> rz[NV], rd[NV];
+    either(q.nt_in, [&](auto nt) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int e = seat.channel(k) < q.EG ? seat.channel(k) : 0;
-      rz[k].load(z + at + e);
-      rd[k].load(d_out + at + e);
-      ry[k].load(y + base + off[k]);
-    }
+      for (int k = 0; k < NV; ++k) {
+        const int e = seat.channel(k) < q.EG ? seat.channel(k) : 0;
+        rz[k].template load<nt.value>(z + at + e);
+        rd[k].template load<nt.value>(d_out + at + e);
+        ry[k].template load<nt.value>(y + base + off[k]);
+      }
+    });
     // sig = silu'(z)'s logistic; kept between the sums and the outputs
     float sig[NV][V], sq = 0.f, ct = 0.f;
 #pragma unroll
@@ -391,8 +405,10 @@ __global__ __launch_bounds__(R::NT) void k_norm_out_bwd(
         dw[k][v] = in ? fmaf(FIRST ? d : d * gate, x * inv, dw[k][v]) : dw[k][v];
       }
       if (in) {
-        store_row<V>(dy + base + off[k], gy);
-        store_row<V>(dz + at + seat.channel(k), gz);
+        either(q.nt_out, [&](auto nt) {
+          store_row<V, nt.value>(dy + base + off[k], gy);
+          store_row<V, nt.value>(dz + at + seat.channel(k), gz);
+        });
       }
     }
   }
@@ -427,9 +443,17 @@ static auto by_row(int64_t EG, bool wide, F&& f) {
 
 // Workgroups: enough to fill the 256 CUs with 2048 threads each (backwards with
 // 1024, whose sums then add up over fewer parts), no more than there is work for.
+// Nontemporal loads where a call moves more than the last-level cache (256 MB)
+// holds, nontemporal stores too where it moves 768 MB and more (below that the
+// cache still takes up much of what is written).  Norm in, E 1024 (plain / loads /
+// both): 101 MB 16.0 / 18.1 / 18.4 us, 403 MB 74.3 / 61.8 / 69.3, 805 MB 150 / 149
+// / 140; backwards 168 MB 33.1 / 33.4 / 35.0, 671 MB 129 / 108 / 118, 1342 MB 260 /
+// 259 / 233.
 template <typename R>
-static Geo geo_of(R, int64_t tokens, int64_t groups, int64_t EG, bool backward) {
+static Geo geo_of(R, int64_t tokens, int64_t groups, int64_t EG, bool backward, int64_t bytes) {
   Geo q{};
+  q.nt_in = bytes >= CACHE_BYTES;
+  q.nt_out = bytes >= 3 * CACHE_BYTES;
   q.tokens = tokens;
   q.groups = (int)groups;
   q.EG = (int)EG;
@@ -443,13 +467,13 @@ static Geo geo_of(R, int64_t tokens, int64_t groups, int64_t EG, bool backward) 
   return q;
 }
 
-static Geo geo_by(int64_t tokens, int64_t groups, int64_t EG, bool wide, bool backward) {
-  return by_row(EG, wide, [&](auto row) { return geo_of(row, tokens, groups, EG, backward); });
+static Geo geo_by(int64_t tokens, int64_t groups, int64_t EG, bool wide, bool backward, int64_t bytes) {
+  return by_row(EG, wide, [&](auto row) { return geo_of(row, tokens, groups, EG, backward, bytes); });
 }
 
 static hipError_t launch_sum_parts(const float* part, int n, int64_t E, float* out0, float* out1,
                                    hipStream_t stream) {
-  hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)((E + 63) / 64), out1 ? 2 : 1), dim3(1024), 0, stream, part,
+  hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)((E + 31) / 32), out1 ? 2 : 1), dim3(1024), 0, stream, part,
                      n, E, out0, out1);
   return hipGetLastError();
 }
@@ -463,10 +487,11 @@ static hipError_t by_call(bool bf16, int64_t EG, bool wide, F&& f) {
 hipError_t launch_norm_in(bool bf16, const float* r, const void* p, const float* s, const float* w,
                           int64_t rows, int64_t E, float eps, float* r_out, void* u,
                           hipStream_t stream) {
+  const int64_t size = bf16 ? 2 : 4;
   return by_call(bf16, E, E % 4 == 0, [&](auto t, auto row) {
     using T = decltype(t);
     using R = decltype(row);
-    const Geo q = geo_of(row, rows, 1, E, false);
+    const Geo q = geo_of(row, rows, 1, E, false, rows * E * (p ? 8 + 2 * size : 4 + size));
     hipLaunchKernelGGL((k_norm_in<T, R>), dim3((unsigned)q.parts), dim3(R::NT), 0, stream, r, (const T*)p,
                        s, w, q, eps, r_out, (T*)u);
     return hipGetLastError();
@@ -474,14 +499,15 @@ hipError_t launch_norm_in(bool bf16, const float* r, const void* p, const float*
 }
 
 size_t norm_in_backward_floats(int64_t rows, int64_t E) {
-  return (size_t)(2 * geo_by(rows, 1, E, E % 4 == 0, true).parts * E);
+  return (size_t)(2 * geo_by(rows, 1, E, E % 4 == 0, true, 0).parts * E);
 }
 
 hipError_t launch_norm_in_backward(bool bf16, const void* du, const float* dr_out, const float* r,
                                    const void* p, const float* s, const float* w, int64_t rows,
                                    int64_t E, float eps, float* dr, float* dp, float* dw, float* ds,
                                    float* ws, hipStream_t stream) {
-  const Geo q = geo_by(rows, 1, E, E % 4 == 0, true);
+  const int64_t size = bf16 ? 2 : 4;
+  const Geo q = geo_by(rows, 1, E, E % 4 == 0, true, rows * E * (8 + size + (dr_out ? 4 : 0) + (s ? 4 + size : 0)));
   if (rows) {
     const hipError_t e = by_call(bf16, E, E % 4 == 0, [&](auto t, auto row) {
       using T = decltype(t);
@@ -504,7 +530,7 @@ hipError_t launch_norm_out(bool bf16, bool gate_first, const float* y, const voi
   return by_call(bf16, EG, heads_wide(DH), [&](auto t, auto row) {
     using T = decltype(t);
     using R = decltype(row);
-    const Geo q = geo_of(row, B * N, groups, EG, false);
+    const Geo q = geo_of(row, B * N, groups, EG, false, B * N * H * DH * (bf16 ? 8 : 12));
     auto go = [&](auto first) {
       hipLaunchKernelGGL((k_norm_out<T, R, first.value>), dim3((unsigned)(q.parts * q.blocks)), dim3(R::NT),
                          0, stream, y, (const T*)z, w, q, Heads{H, N, DH}, eps, (T*)o);
@@ -515,7 +541,7 @@ hipError_t launch_norm_out(bool bf16, bool gate_first, const float* y, const voi
 }
 
 size_t norm_out_backward_floats(int64_t B, int64_t H, int64_t N, int64_t DH, int64_t groups) {
-  return (size_t)(geo_by(B * N, groups, H / groups * DH, heads_wide(DH), true).parts * H * DH);
+  return (size_t)(geo_by(B * N, groups, H / groups * DH, heads_wide(DH), true, 0).parts * H * DH);
 }
 
 hipError_t launch_norm_out_backward(bool bf16, bool gate_first, const void* d_out, const float* y,
@@ -523,7 +549,7 @@ hipError_t launch_norm_out_backward(bool bf16, bool gate_first, const void* d_ou
                                     int64_t DH, int64_t groups, float eps, float* dy, float* dz,
                                     float* dw, float* ws, hipStream_t stream) {
   const int64_t EG = H / groups * DH, tokens = B * N;
-  const Geo q = geo_by(tokens, groups, EG, heads_wide(DH), true);
+  const Geo q = geo_by(tokens, groups, EG, heads_wide(DH), true, tokens * H * DH * (bf16 ? 16 : 20));
   if (tokens) {
     const hipError_t e = by_call(bf16, EG, heads_wide(DH), [&](auto t, auto row) {
       using T = decltype(t);

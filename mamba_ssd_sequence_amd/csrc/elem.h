@@ -64,10 +64,23 @@ __device__ __forceinline__ void either(bool c, F&& f) {
   }
 }
 
+// Element e of an array, by a 32-bit byte offset from a uniform address (less
+// than 2^32 bytes): the offset then needs one register and no 64-bit sum.
+template <typename T>
+__device__ __forceinline__ T* element(T* p, unsigned e) {
+  typedef typename std::conditional<std::is_const<T>::value, const char, char>::type byte;
+  return reinterpret_cast<T*>(reinterpret_cast<byte*>(p) + e * (unsigned)sizeof(T));
+}
+
 // The last-level cache.
 constexpr int64_t CACHE_BYTES = (int64_t)256 << 20;
 
+// Pieces of 4 elements, at the alignment of one: rows of any width are read and
+// written in whole pieces (the hardware takes them at any element's address).
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+typedef bf16x4 bf16x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
 // V consecutive elements of a row as they are stored.  or_else(): the elements,
 // or one bit pattern for all of them (fp32's upper half) where `in` is false;
@@ -81,7 +94,7 @@ template <> struct Raw<uint16_t, 4> {
     r.y = in ? r.y : other;
   }
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r.x), "+v"(r.y)); }
-  template <bool NT = false> __device__ __forceinline__ void load(const uint16_t* p) { r = load_as<NT, u32x2>(p); }
+  template <bool NT = false> __device__ __forceinline__ void load(const uint16_t* p) { r = load_as<NT, u32x2_any>(p); }
   __device__ __forceinline__ float get(int v) const {
     const unsigned w = v < 2 ? r.x : r.y;
     return __uint_as_float(v % 2 ? w & 0xffff0000u : w << 16);
@@ -94,7 +107,7 @@ template <> struct Raw<float, 4> {
     for (int v = 0; v < 4; ++v) r[v] = in ? r[v] : __uint_as_float(other << 16);
   }
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
-  template <bool NT = false> __device__ __forceinline__ void load(const float* p) { r = load_as<NT, f32x4>(p); }
+  template <bool NT = false> __device__ __forceinline__ void load(const float* p) { r = load_as<NT, f32x4_any>(p); }
   __device__ __forceinline__ float get(int v) const { return r[v]; }
 };
 template <> struct Raw<uint16_t, 1> {
@@ -115,17 +128,18 @@ template <> struct Raw<float, 1> {
 template <int V, bool NT = false>
 __device__ __forceinline__ void store_row(float* p, const float (&v)[V]) {
   if constexpr (V == 4)
-    store_as<NT>(p, f32x4{v[0], v[1], v[2], v[3]});
+    store_as<NT, f32x4_any>(p, f32x4{v[0], v[1], v[2], v[3]});
   else
-    store_as<NT>(p, v[0]);
+    store_as<NT, float>(p, v[0]);
 }
 
 template <int V, bool NT = false>
 __device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[V]) {
   if constexpr (V == 4)
-    store_as<NT>(p, bf16x4{f32_to_bf16(v[0]), f32_to_bf16(v[1]), f32_to_bf16(v[2]), f32_to_bf16(v[3])});
+    store_as<NT, bf16x4_any>(
+        p, bf16x4{f32_to_bf16(v[0]), f32_to_bf16(v[1]), f32_to_bf16(v[2]), f32_to_bf16(v[3])});
   else
-    store_as<NT>(p, f32_to_bf16(v[0]));
+    store_as<NT, __bf16>(p, f32_to_bf16(v[0]));
 }
 
 }  // namespace ssd

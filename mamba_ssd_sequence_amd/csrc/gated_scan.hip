@@ -118,10 +118,11 @@ __global__ __launch_bounds__(256) void k_clear_words(uint4* p, int64_t n) {
 
 // Steps (P, U) of the groups of a wave along its tokens (reverse: from the last
 // group to the first) -> for each group the composition of the groups before it;
-// the whole wave's composition goes to LDS.
+// the whole wave's composition goes to LDS, channel c on (lanes without channels
+// of their own have channel 0's values, and write them once more).
 template <typename TL, bool REVERSE>
-__device__ __forceinline__ void scan_groups(float (&P)[TL::V], float (&U)[TL::V], int lane, float* sP,
-                                            float* sU) {
+__device__ __forceinline__ void scan_groups(float (&P)[TL::V], float (&U)[TL::V], int lane, int c,
+                                            float* sP, float* sU) {
   const int tg = REVERSE ? TL::TG - 1 - lane / TL::LPR : lane / TL::LPR;
   auto before = [](float x, int groups) {
     return REVERSE ? __shfl_down(x, groups * TL::LPR, WAVE) : __shfl_up(x, groups * TL::LPR, WAVE);
@@ -137,7 +138,6 @@ __device__ __forceinline__ void scan_groups(float (&P)[TL::V], float (&U)[TL::V]
       }
     }
   if (tg == TL::TG - 1) {
-    const int c = lane % TL::LPR * TL::V;
     store_row<TL::V>(sP + c, P);
     store_row<TL::V>(sU + c, U);
   }
@@ -239,26 +239,33 @@ __device__ __forceinline__ int take_tile(int tiles, unsigned* counter) {
   return __builtin_amdgcn_readfirstlane(mine);
 }
 
+// The channels of a slab: `width` of them (a multiple of V; a slab's lanes past
+// them are idle) from `start`.  Pieces of 4 that would pass the head's last
+// channel are moved back to end with it, and a slab that would begin with fewer
+// than 4 channels left begins 4 before the end: lanes or slabs then share
+// channels, compute the same values for them and write them twice.
+template <typename TL>
+__device__ __forceinline__ int slab_start(int slab, int width, int DH) {
+  return slab * width < DH - TL::V ? slab * width : DH - TL::V;
+}
+
 // Where a workgroup and a thread are: every array is addressed from a uniform
-// pointer at the tile's first row by 32-bit offsets (at most 512 rows of at most
-// SSD_GATED_MAX = 2^20 channels), so that offsets past 2^32 elements cost no
-// registers.
+// pointer at the tile's first row by 32-bit byte offsets (at most 512 rows of at
+// most SSD_GATED_MAX = 2^20 channels, more rows only of 32 channels and less), so
+// that offsets past 2^32 elements cost no registers.
 template <typename TL>
 struct Spot {
-  int64_t base, state;  // element of the tile's first row and channel; of the head's state
-  int tok, rows, c;     // the thread's first token in the tile, the tile's tokens, its channel
-  bool live;            // the channel exists
-  __device__ __forceinline__ Spot(int64_t hs, int tile, int64_t N, int DH, int slabs) {
-    const int64_t bh = hs / slabs;
-    const int slab = (int)(hs - bh * slabs), lane = threadIdx.x % WAVE;
+  int64_t base;      // element of the tile's first row and the slab's first channel
+  int tok, rows, c;  // the thread's first token in the tile, the tile's tokens, its channel in the slab
+  bool live;         // it has channels of its own
+  __device__ __forceinline__ Spot(int64_t bh, int start, int tile, int64_t N, int DH, int width) {
+    const int lane = threadIdx.x % WAVE, nominal = lane % TL::LPR * TL::V;
     const int64_t left = N - (int64_t)tile * TL::TOKENS;
     rows = left < TL::TOKENS ? (int)left : TL::TOKENS;
-    state = bh * DH + slab * TL::C;
-    base = (bh * N + (int64_t)tile * TL::TOKENS) * DH + slab * TL::C;
+    base = (bh * N + (int64_t)tile * TL::TOKENS) * DH + start;
     tok = (threadIdx.x / WAVE * TL::TG + lane / TL::LPR) * TL::TT;
-    c = lane % TL::LPR * TL::V;
-    live = slab * TL::C + c < DH;
-    if (!live) c = 0;
+    live = nominal < width && start + nominal < DH;
+    c = !live ? 0 : start + nominal + TL::V <= DH ? nominal : DH - TL::V - start;
   }
   // offset of row tok + i, or of the last row
   __device__ __forceinline__ unsigned at(int i, int DH) const {
@@ -269,20 +276,22 @@ struct Spot {
 template <typename T, int SCALE, bool GATE, typename TL>
 __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan(
     const T* __restrict__ x, const T* __restrict__ A, const T* __restrict__ I,
-    const float* __restrict__ h0, int64_t N, int DH, int slabs, int heads, int tiles, int runs,
+    const float* __restrict__ h0, int64_t N, int DH, int width, int slabs, int heads, int tiles, int runs,
     bool nt_out, float* __restrict__ y, float* __restrict__ hf, unsigned* counters, word_t* words) {
   constexpr int V = TL::V, TT = TL::TT, C = TL::C;
   __shared__ Joint<TL> j;
   const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
   const int hs = blockIdx.x % heads;  // head and slab
+  const int start = slab_start<TL>(hs % slabs, width, DH);
+  const int64_t bh = hs / slabs, state = bh * DH + start;  // the head, its state's first channel here
   const int taken = take_tile(tiles, counters + hs);
-  const bool exists = lane < C && hs % slabs * C + lane < DH;
+  const bool exists = lane < width && start + lane < DH;
   float enter = 0.f;  // in the first wave: the state entering the sequence, then each next tile
-  if (wave == 0 && exists && h0) enter = h0[(int64_t)(hs / slabs) * DH + hs % slabs * C + lane];
+  if (wave == 0 && exists && h0) enter = h0[state + lane];
   for (int k = 0; k < runs; ++k) {
   const int tile = taken + k;
   asm("" : "+s"(DH));  // a tile's offsets are not worth registers over the loop
-  const Spot<TL> sp(hs, tile, N, DH, slabs);
+  const Spot<TL> sp(bh, start, tile, N, DH, width);
   const T *xt = x + sp.base, *At = A + sp.base, *It = I + sp.base;
   float* yt = y + sp.base;
 
@@ -290,9 +299,9 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan(
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
     const unsigned at = sp.at(i, DH);
-    rA[i].template load<true>(At + at);
-    if constexpr (GATE) rI[i].template load<true>(It + at);
-    rx[i].template load<true>(xt + at);
+    rA[i].template load<true>(element(At, at));
+    if constexpr (GATE) rI[i].template load<true>(element(It, at));
+    rx[i].template load<true>(element(xt, at));
   }
   float a[TT][V], u[TT][V], P[V], U[V];
 #pragma unroll
@@ -314,7 +323,7 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan(
       P[v] *= a[i][v];
     }
   }
-  scan_groups<TL, false>(P, U, lane, j.P + wave * C, j.U + wave * C);
+  scan_groups<TL, false>(P, U, lane, sp.c, j.P + wave * C, j.U + wave * C);
   __syncthreads();
   enter = join_tiles<TL, false>(j, wave, lane, exists, tiles > 1 ? tile : 0, tiles, enter,
                                 words + hs * slab_words(tiles, C));
@@ -327,8 +336,8 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan(
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], u[i][v]);
     if (sp.live && sp.tok + i < sp.rows) {
-      either(nt_out, [&](auto nt) { store_row<V, nt.value>(yt + sp.at(i, DH), h); });
-      if (last && sp.tok + i == sp.rows - 1) store_row<V>(hf + sp.state + sp.c, h);
+      either(nt_out, [&](auto nt) { store_row<V, nt.value>(element(yt, sp.at(i, DH)), h); });
+      if (last && sp.tok + i == sp.rows - 1) store_row<V>(hf + state + sp.c, h);
     }
   }
   }
@@ -343,21 +352,23 @@ template <typename T, int SCALE, bool GATE, typename TL>
 __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
     const T* __restrict__ x, const T* __restrict__ A, const T* __restrict__ I,
     const float* __restrict__ h0, const float* __restrict__ y, const float* __restrict__ dy,
-    const float* __restrict__ dlast, int64_t N, int DH, int slabs, int heads, int tiles, int runs,
+    const float* __restrict__ dlast, int64_t N, int DH, int width, int slabs, int heads, int tiles, int runs,
     bool nt_out, float* __restrict__ dx, float* __restrict__ dA, float* __restrict__ dI,
     float* __restrict__ dh0, unsigned* counters, word_t* words) {
   constexpr int V = TL::V, TT = TL::TT, C = TL::C;
   __shared__ Joint<TL> j;
   const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
   const int hs = blockIdx.x % heads;
+  const int start = slab_start<TL>(hs % slabs, width, DH);
+  const int64_t bh = hs / slabs, state = bh * DH + start;
   const int taken = take_tile(tiles, counters + hs);
-  const bool exists = lane < C && hs % slabs * C + lane < DH;
+  const bool exists = lane < width && start + lane < DH;
   float enter = 0.f;  // in the first wave: d_final_state, then the c that leaves each tile
-  if (wave == 0 && exists && dlast) enter = dlast[(int64_t)(hs / slabs) * DH + hs % slabs * C + lane];
+  if (wave == 0 && exists && dlast) enter = dlast[state + lane];
   for (int k = 0; k < runs; ++k) {
   const int order = taken + k, tile = tiles * runs - 1 - order;
   asm("" : "+s"(DH));  // a tile's offsets are not worth registers over the loop
-  const Spot<TL> sp(hs, tile, N, DH, slabs);
+  const Spot<TL> sp(bh, start, tile, N, DH, width);
   const T *xt = x + sp.base, *At = A + sp.base, *It = I + sp.base;
   const float *dyt = dy + sp.base, *yt = y + sp.base - DH;  // yt: a row before, the states before each token
   float *dxt = dx + sp.base, *dAt = dA + sp.base, *dIt = dI + sp.base;
@@ -367,18 +378,18 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
   Raw<float, V> rd[TT], rp[TT], r0;
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
-    rA[i].template load<true>(At + sp.at(i, DH));
-    rd[i].template load<true>(dyt + sp.at(i, DH));
+    rA[i].template load<true>(element(At, sp.at(i, DH)));
+    rd[i].template load<true>(element(dyt, sp.at(i, DH)));
   }
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
     const unsigned at = sp.at(i, DH);
-    rx[i].template load<true>(xt + at);
-    if constexpr (GATE) rI[i].template load<true>(It + at);
+    rx[i].template load<true>(element(xt, at));
+    if constexpr (GATE) rI[i].template load<true>(element(It, at));
     // the row before; before the sequence's first row there is none, and its own is read without use
-    rp[i].template load<true>(yt + (tile == 0 && at < (unsigned)DH ? at + DH : at));
+    rp[i].template load<true>(element(yt, tile == 0 && at < (unsigned)DH ? at + DH : at));
   }
-  if (tile == 0 && h0) r0.load(h0 + sp.state + sp.c);
+  if (tile == 0 && h0) r0.load(h0 + state + sp.c);
   float P[V], U[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -397,7 +408,7 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
       P[v] *= a;
     }
   }
-  scan_groups<TL, true>(P, U, lane, j.P + wave * C, j.U + wave * C);
+  scan_groups<TL, true>(P, U, lane, sp.c, j.P + wave * C, j.U + wave * C);
   __syncthreads();
   enter = join_tiles<TL, true>(j, wave, lane, exists, tiles > 1 ? order : 0, tiles, enter,
                                words + hs * slab_words(tiles, C));
@@ -429,11 +440,11 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
     }
     const unsigned at = sp.at(i, DH);
     either(nt_out, [&](auto nt) {
-      store_row<V, nt.value>(dxt + at, ox);
-      store_row<V, nt.value>(dAt + at, oA);
-      if constexpr (GATE) store_row<V, nt.value>(dIt + at, oI);
+      store_row<V, nt.value>(element(dxt, at), ox);
+      store_row<V, nt.value>(element(dAt, at), oA);
+      if constexpr (GATE) store_row<V, nt.value>(element(dIt, at), oI);
     });
-    if (i == 0 && first && dh0) store_row<V>(dh0 + sp.state + sp.c, carry);
+    if (i == 0 && first && dh0) store_row<V>(dh0 + state + sp.c, carry);
   }
   }
 }
@@ -465,12 +476,11 @@ static hipError_t by_type(bool bf16, int scale, F&& f) {
   return bf16 ? with(uint16_t{}) : with(float{});
 }
 
-// The tile of a call: 4 channels a lane where rows are whole 16-byte (bf16:
-// 8-byte) pieces, d_h a multiple of 4, 64 channels a tile (32 when the head has
-// no more); else a channel a lane, 16 a tile.
+// The tile of a call: 4 channels a lane, 64 a tile (32 when the head has no
+// more); heads of fewer than 4 channels a channel a lane, 4 a tile.
 enum { WIDE64, WIDE32, NARROW };
-static int tile_kind(int64_t DH) { return DH % 4 ? NARROW : DH > 32 ? WIDE64 : WIDE32; }
-constexpr int kind_lpr(int k) { return k == WIDE32 ? 8 : 16; }
+static int tile_kind(int64_t DH) { return DH < 4 ? NARROW : DH > 32 ? WIDE64 : WIDE32; }
+constexpr int kind_lpr(int k) { return k == WIDE64 ? 16 : k == WIDE32 ? 8 : 4; }
 constexpr int kind_v(int k) { return k == NARROW ? 1 : 4; }
 
 // Tokens a thread: what its registers hold (16 waves of 128 a CU).
@@ -487,7 +497,8 @@ constexpr int BWD_TOKENS = 4;
 // of 2048 tokens: 121 us against 125).
 struct Split {
   int64_t slabs, heads, tiles;  // tiles: those that workgroups of one head share out
-  int waves, runs, C;           // runs: tiles that a workgroup takes one after the other (then tiles = 1)
+  int waves, runs, C, width;    // runs: tiles that a workgroup takes one after the other (then tiles = 1);
+                                // width: channels of a slab, at most the tile's C
   // floats: the counters, padded, then the words
   size_t counters() const { return (size_t)((heads + 63) & ~(int64_t)63); }
   size_t floats() const { return tiles > 1 ? counters() + (size_t)(heads * slab_words(tiles, C)) * 2 : 0; }
@@ -496,13 +507,14 @@ struct Split {
 static Split split_of(int64_t BH, int64_t N, int64_t DH, int tokens) {
   const int k = tile_kind(DH), lpr = kind_lpr(k), C = lpr * kind_v(k);
   const int64_t slabs = (DH + C - 1) / C, heads = BH * slabs;
+  const int even = (int)((DH + slabs - 1) / slabs), width = k == NARROW ? even : (even + 3) / 4 * 4;
   auto tiles = [&](int waves) {
     const int64_t per = (int64_t)waves * (WAVE / lpr) * tokens;
     return (N + per - 1) / per;
   };
-  if (heads * tiles(16) <= 512) return {slabs, heads, tiles(16), 16, 1, C};
-  if (heads >= 512) return {slabs, heads, 1, 8, (int)tiles(8), C};
-  return {slabs, heads, tiles(8), 8, 1, C};
+  if (heads * tiles(16) <= 512) return {slabs, heads, tiles(16), 16, 1, C, width};
+  if (heads >= 512) return {slabs, heads, 1, 8, (int)tiles(8), C, width};
+  return {slabs, heads, tiles(8), 8, 1, C, width};
 }
 
 // for either element type
@@ -563,7 +575,7 @@ hipError_t launch_gated_scan(bool bf16, int scale, const void* x, const void* A,
     using TL = Tile<kind_v(k.value), kind_lpr(k.value), nw.value, fwd_tokens(sizeof(T) == 2)>;
     hipLaunchKernelGGL((k_gated_scan<T, sc.value, g.value, TL>), dim3((unsigned)(s.heads * s.tiles)),
                        dim3(TL::NW * WAVE), 0, stream, (const T*)x, (const T*)A, (const T*)I, h0, N,
-                       (int)DH, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs, nt_out(bytes), y, hf, (unsigned*)ws,
+                       (int)DH, s.width, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs, nt_out(bytes), y, hf, (unsigned*)ws,
                        (word_t*)(ws + s.counters()));
     return hipGetLastError();
   });
@@ -594,7 +606,7 @@ hipError_t launch_gated_scan_backward(bool bf16, int scale, const void* x, const
     using TL = Tile<kind_v(k.value), kind_lpr(k.value), nw.value, BWD_TOKENS>;
     hipLaunchKernelGGL((k_gated_scan_bwd<T, sc.value, g.value, TL>), dim3((unsigned)(s.heads * s.tiles)),
                        dim3(TL::NW * WAVE), 0, stream, (const T*)x, (const T*)A, (const T*)I, h0, y, dy,
-                       dlast, N, (int)DH, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs, nt_out(bytes), dx, dA, dI, dh0,
+                       dlast, N, (int)DH, s.width, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs, nt_out(bytes), dx, dA, dI, dh0,
                        (unsigned*)ws, (word_t*)(ws + s.counters()));
     return hipGetLastError();
   });

@@ -144,6 +144,12 @@ SCAN = [
     (1, 1, 40000, 3, "bf16", True, True, False),
     (1, 14, 20000, 32, "bf16", False, True, True),
     (1, 12, 12000, 64, "f32", True, True, False),
+    # heads whose last piece or slab is moved back: 4 n + 1 .. 3 channels, one more than a slab, more slabs than even
+    (1, 2, 300, 5, "bf16", True, True, False),
+    (2, 1, 300, 34, "bf16", True, True, True),
+    (1, 1, 700, 67, "f32", True, True, False),
+    (1, 1, 130, 1217, "bf16", True, True, False),
+    (1, 2, 600, 2, "f32", True, True, False),
     # heads enough to take a head's tiles one after the other
     (65, 8, 600, 64, "bf16", True, True, True),
     (65, 8, 300, 17, "f32", False, True, False),
@@ -302,7 +308,8 @@ def norm_in_inputs(R, E, dtype, seed):
 NORM_IN = [(1, 1, "f32"), (3, 7, "bf16"), (5, 64, "f32"), (70, 33, "bf16"), (9, 512, "bf16"), (4, 1000, "f32"),
            (33, 1024, "bf16"), (2, 1025, "bf16"), (6, 2048, "bf16"), (300, 260, "f32"), (3, 4096, "f32"),
            (2, 5001, "bf16"), (2, 16384, "bf16"), (1, 20000, "f32"), (2, 32768, "bf16"), (1, 32767, "f32"),
-           (2500, 64, "bf16"), (5000, 36, "f32")]
+           (2500, 64, "bf16"), (5000, 36, "f32"),
+           (7, 5, "f32"), (7, 6, "bf16"), (40, 129, "f32"), (3, 9001, "bf16"), (2, 2, "bf16")]
 
 
 @pytest.mark.parametrize("R,E,dtype", NORM_IN)
@@ -355,7 +362,9 @@ NORM_OUT = [(1, 1, 1, 1, 1, "f32"), (2, 3, 5, 7, 1, "bf16"), (2, 3, 5, 7, 3, "f3
             (3, 2, 11, 64, 2, "bf16"), (1, 16, 33, 64, 1, "bf16"), (1, 16, 33, 64, 16, "f32"), (2, 32, 3, 64, 4, "bf16"),
             (5, 32, 1, 64, 1, "bf16"), (1, 12, 9, 33, 1, "bf16"), (1, 64, 2, 128, 1, "f32"), (2, 20, 3, 36, 5, "bf16"),
             (1, 1, 700, 64, 1, "bf16"), (1, 512, 2, 64, 1, "bf16"), (1, 7, 2, 4681, 1, "f32"), (130, 2, 20, 32, 2, "f32"),
-            (1, 1, 3000, 4, 1, "bf16"), (2, 600, 2, 64, 2, "f32")]
+            (1, 1, 3000, 4, 1, "bf16"), (2, 600, 2, 64, 2, "f32"),
+            (2, 9, 7, 5, 1, "bf16"), (2, 9, 7, 6, 9, "f32"), (3, 8, 40, 33, 2, "bf16"), (2, 5, 3, 3, 1, "bf16"), (1, 500, 3, 2, 1, "f32"),
+            (1, 6553, 1, 5, 1, "bf16"), (2, 8, 9, 128, 8, "bf16"), (1, 64, 2, 127, 2, "f32")]
 
 
 def norm_out_inputs(B, H, N, d, dtype, seed):

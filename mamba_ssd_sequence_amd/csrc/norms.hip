@@ -18,6 +18,12 @@
 // of 4 channels each, of which the last is moved back to end with the head.  Its
 // first channels are then also the piece's before it; they count once in the
 // row's sums, and are computed and written twice with the same values.
+//
+// Rows of more than 2048 pieces (8192 channels) do not fit that way: backwards a
+// thread would hold 128 values and more, and spilled (16384 channels, 1024 rows:
+// 216 us).  A workgroup then walks along a row twice, forwards; backwards one
+// kernel leaves each row's two means, and another takes blocks of 256 pieces down
+// the rows (90 us, 3.7 TB/s of the bytes that have to move).
 #include "block.h"
 #include "common.h"
 #include "elem.h"
@@ -31,9 +37,6 @@ struct Row {
   static constexpr int V = V_, TPR = TPR_, NV = NV_;
   static constexpr int NT = TPR > 512 ? TPR : 512;  // threads of a workgroup
   static constexpr int SLOTS = NT / TPR;            // rows it holds
-  // What registers hold: the weights up to 8 channels a thread, the row up to
-  // 16.  Longer rows read them again (from the L2).
-  static constexpr bool HOLD_W = NV * V <= 8, HOLD_ROW = NV * V <= 16;
 };
 
 // Which rows a workgroup takes: `gpw` groups of `tpw` tokens at a time; there
@@ -46,6 +49,22 @@ struct Geo {
   int gpw, tpw, blocks, parts;
   bool nt_in, nt_out;  // nontemporal loads, stores
 };
+
+// A piece of a group's row: its first channel there, the head it is in, and how
+// many of its channels are not its own (V: there is no such piece).
+struct Piece {
+  unsigned at;
+  int head, skip;
+};
+
+template <int V>
+__device__ __forceinline__ Piece piece_of(int i, const Geo& q) {
+  const int each = (q.width + V - 1) / V;
+  const bool is = i < q.pieces;
+  const int head = is ? i / each : 0;
+  const int c = is ? (i - head * each) * V : 0, moved = c < q.width - V ? c : q.width - V;
+  return {(unsigned)(head * q.width + moved), head, is ? c - moved : V};
+}
 
 // A thread's place: its row's group and token, its pieces' channels.
 template <typename R>
@@ -63,36 +82,18 @@ struct Seat {
     g = (blockIdx.x - part * q.blocks) * q.gpw + slot % q.gpw;
     seated = g < q.groups && slot / q.gpw < q.tpw;
     if (!seated) g = 0;
-    const int each = (q.width + R::V - 1) / R::V;
 #pragma unroll
     for (int k = 0; k < R::NV; ++k) {
-      const int piece = k * R::TPR + lane;
-      const bool is = piece < q.pieces;
-      head[k] = is ? piece / each : 0;
-      const int c = is ? (piece - head[k] * each) * R::V : 0, moved = c < q.width - R::V ? c : q.width - R::V;
-      at[k] = head[k] * q.width + moved;
-      skip[k] = is ? c - moved : R::V;
+      const Piece p = piece_of<R::V>(k * R::TPR + lane, q);
+      at[k] = p.at;
+      head[k] = p.head;
+      skip[k] = p.skip;
     }
   }
   __device__ __forceinline__ bool is(int k) const { return skip[k] < R::V; }
   // the piece's place among the pieces of the row
   __device__ __forceinline__ int nominal(int k) const { return (k * R::TPR + lane) * R::V; }
 };
-
-// A long row's pieces are taken one after the other: their loads stay where they
-// are written, or the registers that all of them need would go to scratch.
-template <typename R>
-__device__ __forceinline__ void piece_by_piece() {
-  if constexpr (!R::HOLD_W) __builtin_amdgcn_sched_barrier(0);
-}
-
-// The same address, as one that nothing is known of: what is read from it is
-// not kept from an earlier read.
-template <typename P>
-__device__ __forceinline__ P* afresh(P* p) {
-  asm volatile("" : "+s"(p));
-  return p;
-}
 
 // Sums of a and b over the TPR threads of each row.  With more than a wave a
 // row, through LDS: `turn` alternates between two sets of slots, so that one
@@ -134,7 +135,6 @@ __global__ __launch_bounds__(R::NT) void k_norm_in(const float* __restrict__ r, 
   const Seat<R> seat(q);
   const float inv_n = 1.f / (float)q.EG;
   Raw<float, V> rw[NV], rs[NV];
-  if constexpr (R::HOLD_W)
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       rw[k].load(element(w, seat.at[k]));
@@ -154,13 +154,9 @@ __global__ __launch_bounds__(R::NT) void k_norm_in(const float* __restrict__ r, 
         if (p) rp[k].template load<nt.value>(element(p + at, seat.at[k]));
       }
     });
-    if constexpr (!R::HOLD_W) s = s ? afresh(s) : s;
     float x[NV][V], sum = 0.f, none = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      piece_by_piece<R>();
-      if constexpr (!R::HOLD_W)
-        if (s) rs[k].load(element(s, seat.at[k]));
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float y = rr[k].get(v);
@@ -173,11 +169,8 @@ __global__ __launch_bounds__(R::NT) void k_norm_in(const float* __restrict__ r, 
     }
     row_sums<R>(sum, none, turn);
     const float inv = inv_rms(sum, inv_n, eps);
-    if constexpr (!R::HOLD_W) w = afresh(w);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      piece_by_piece<R>();
-      if constexpr (!R::HOLD_W) rw[k].load(element(w, seat.at[k]));
 #pragma unroll
       for (int v = 0; v < V; ++v) x[k][v] = x[k][v] * inv * rw[k].get(v);
       if (live && seat.is(k))
@@ -217,7 +210,7 @@ __device__ __forceinline__ void store_part(const Seat<R>& seat, const Geo& q, co
   }
 }
 
-template <typename T, typename R>
+template <typename T, typename R, bool SCALED, bool ADDED>
 __global__ __launch_bounds__(R::NT) void k_norm_in_bwd(
     const T* __restrict__ du, const float* __restrict__ dr_out, const float* __restrict__ r,
     const T* __restrict__ p, const float* __restrict__ s, const float* __restrict__ w, Geo q, float eps,
@@ -229,10 +222,8 @@ __global__ __launch_bounds__(R::NT) void k_norm_in_bwd(
   float dw[NV][V], ds[NV][V];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    if constexpr (R::HOLD_W) {
-      rw[k].load(element(w, seat.at[k]));
-      if (s) rs[k].load(element(s, seat.at[k]));
-    }
+    rw[k].load(element(w, seat.at[k]));
+    if constexpr (SCALED) rs[k].load(element(s, seat.at[k]));
 #pragma unroll
     for (int v = 0; v < V; ++v) dw[k][v] = ds[k][v] = 0.f;
   }
@@ -243,23 +234,18 @@ __global__ __launch_bounds__(R::NT) void k_norm_in_bwd(
     const int64_t at = (live ? row : q.tokens - 1) * q.EG;
     Raw<float, V> rr[NV], ro[NV];
     Raw<T, V> rp[NV], rd[NV];
-    either(q.nt_in && R::HOLD_ROW, [&](auto nt) {
+    either(q.nt_in, [&](auto nt) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         rr[k].template load<nt.value>(element(r + at, seat.at[k]));
         rd[k].template load<nt.value>(element(du + at, seat.at[k]));
-        if constexpr (R::HOLD_ROW) {
-          if (dr_out) ro[k].template load<nt.value>(element(dr_out + at, seat.at[k]));
-          if (s) rp[k].template load<nt.value>(element(p + at, seat.at[k]));
-        }
+        if constexpr (ADDED) ro[k].template load<nt.value>(element(dr_out + at, seat.at[k]));
+        if constexpr (SCALED) rp[k].template load<nt.value>(element(p + at, seat.at[k]));
       }
     });
-    if constexpr (!R::HOLD_W) w = afresh(w);
     float sq = 0.f, cr = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      piece_by_piece<R>();
-      if constexpr (!R::HOLD_W) rw[k].load(element(w, seat.at[k]));
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float y = rr[k].get(v), c = rd[k].get(v) * rw[k].get(v);
@@ -269,35 +255,16 @@ __global__ __launch_bounds__(R::NT) void k_norm_in_bwd(
     }
     row_sums<R>(sq, cr, turn);
     const float inv = inv_rms(sq, inv_n, eps), m = inv * inv * inv * (cr * inv_n);
-    if constexpr (!R::HOLD_W) {
-      w = afresh(w);
-      s = s ? afresh(s) : s;
-    }
-    if constexpr (!R::HOLD_ROW) {
-      r = afresh(r);
-      du = afresh(du);
-    }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      piece_by_piece<R>();
-      if constexpr (!R::HOLD_W) {
-        rw[k].load(element(w, seat.at[k]));
-        if (s) rs[k].load(element(s, seat.at[k]));
-      }
-      if constexpr (!R::HOLD_ROW) {
-        rr[k].load(element(r + at, seat.at[k]));
-        rd[k].load(element(du + at, seat.at[k]));
-        if (dr_out) ro[k].load(element(dr_out + at, seat.at[k]));
-        if (s) rp[k].load(element(p + at, seat.at[k]));
-      }
       float g[V], h[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float y = rr[k].get(v), d = rd[k].get(v);
         g[v] = fmaf(-m, y, inv * (d * rw[k].get(v)));
-        if (dr_out) g[v] += ro[k].get(v);
+        if constexpr (ADDED) g[v] += ro[k].get(v);
         dw[k][v] = live ? fmaf(d, y * inv, dw[k][v]) : dw[k][v];
-        if (s) {
+        if constexpr (SCALED) {
           h[v] = rs[k].get(v) * g[v];
           ds[k][v] = live ? fmaf(g[v], rp[k].get(v), ds[k][v]) : ds[k][v];
         }
@@ -305,12 +272,12 @@ __global__ __launch_bounds__(R::NT) void k_norm_in_bwd(
       if (live && seat.is(k))
         either(q.nt_out, [&](auto nt) {
           store_row<V, nt.value>(element(dr + at, seat.at[k]), g);
-          if (s) store_row<V, nt.value>(element(dp + at, seat.at[k]), h);
+          if constexpr (SCALED) store_row<V, nt.value>(element(dp + at, seat.at[k]), h);
         });
     }
   }
   store_part<R>(seat, q, dw, part + (int64_t)seat.part * q.EG);
-  if (s) store_part<R>(seat, q, ds, part + (int64_t)(q.parts + seat.part) * q.EG);
+  if constexpr (SCALED) store_part<R>(seat, q, ds, part + (int64_t)(q.parts + seat.part) * q.EG);
 }
 
 // out[i][e] = sum over n partial rows of set i, e < E: a workgroup takes 32
@@ -355,7 +322,7 @@ __global__ __launch_bounds__(R::NT) void k_norm_out(const float* __restrict__ y,
   int64_t off[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    if constexpr (R::HOLD_W) rw[k].load(element(w + e0, seat.at[k]));
+    rw[k].load(element(w + e0, seat.at[k]));
     off[k] = (h0 + seat.head[k]) * hd.N * hd.DH + ((int)seat.at[k] - seat.head[k] * q.width);
   }
   int turn = 0;
@@ -384,17 +351,26 @@ __global__ __launch_bounds__(R::NT) void k_norm_out(const float* __restrict__ y,
       }
     row_sums<R>(sum, none, turn);
     const float inv = inv_rms(sum, inv_n, eps);
-    if constexpr (!R::HOLD_W) w = afresh(w);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      piece_by_piece<R>();
-      if constexpr (!R::HOLD_W) rw[k].load(element(w + e0, seat.at[k]));
 #pragma unroll
       for (int v = 0; v < V; ++v) x[k][v] = x[k][v] * inv * rw[k].get(v);
       if (live && seat.is(k))
         either(q.nt_out, [&](auto nt) { store_row<V, nt.value>(element(o + at, seat.at[k]), x[k]); });
     }
   }
+}
+
+// One channel's gradients: k = inv, m = k^3 mean(c x).
+template <bool FIRST>
+__device__ __forceinline__ void norm_out_slopes(float z, float y, float d, float w, float inv, float m,
+                                                float& dy, float& dz, float& dw) {
+  const float sig = sigmoid_v(z), gate = z * sig, slope = sig * fmaf(z, 1.f - sig, 1.f);
+  const float c = d * w, x = FIRST ? y * gate : y;
+  const float dx = fmaf(-m, x, inv * (FIRST ? c : c * gate));
+  dy = FIRST ? dx * gate : dx;
+  dz = FIRST ? dx * y * slope : c * (y * inv) * slope;
+  dw = fmaf(FIRST ? d : d * gate, x * inv, dw);
 }
 
 template <typename T, typename R, bool FIRST>
@@ -412,7 +388,7 @@ __global__ __launch_bounds__(R::NT) void k_norm_out_bwd(
   int64_t off[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    if constexpr (R::HOLD_W) rw[k].load(element(w + e0, seat.at[k]));
+    rw[k].load(element(w + e0, seat.at[k]));
     off[k] = (h0 + seat.head[k]) * hd.N * hd.DH + ((int)seat.at[k] - seat.head[k] * q.width);
 #pragma unroll
     for (int v = 0; v < V; ++v) dw[k][v] = 0.f;
@@ -424,7 +400,7 @@ __global__ __launch_bounds__(R::NT) void k_norm_out_bwd(
     const int64_t base = hd.base(token), at = token * E + e0;
     Raw<float, V> ry[NV];
     Raw<T, V> rz[NV], rd[NV];
-    either(q.nt_in && R::HOLD_ROW, [&](auto nt) {
+    either(q.nt_in, [&](auto nt) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         rz[k].template load<nt.value>(element(z + at, seat.at[k]));
@@ -432,12 +408,9 @@ __global__ __launch_bounds__(R::NT) void k_norm_out_bwd(
         ry[k].template load<nt.value>(y + base + off[k]);
       }
     });
-    if constexpr (!R::HOLD_W) w = afresh(w);
     float sq = 0.f, ct = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      piece_by_piece<R>();
-      if constexpr (!R::HOLD_W) rw[k].load(element(w + e0, seat.at[k]));
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float zv = rz[k].get(v), yv = ry[k].get(v), gate = zv * sigmoid_v(zv);
@@ -448,31 +421,14 @@ __global__ __launch_bounds__(R::NT) void k_norm_out_bwd(
     }
     row_sums<R>(sq, ct, turn);
     const float inv = inv_rms(sq, inv_n, eps), m = inv * inv * inv * (ct * inv_n);
-    if constexpr (!R::HOLD_W) w = afresh(w);
-    if constexpr (!R::HOLD_ROW) {
-      y = afresh(y);
-      z = afresh(z);
-      d_out = afresh(d_out);
-    }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      piece_by_piece<R>();
-      if constexpr (!R::HOLD_W) rw[k].load(element(w + e0, seat.at[k]));
-      if constexpr (!R::HOLD_ROW) {
-        rz[k].load(element(z + at, seat.at[k]));
-        rd[k].load(element(d_out + at, seat.at[k]));
-        ry[k].load(y + base + off[k]);
-      }
       float gy[V], gz[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float zv = rz[k].get(v), yv = ry[k].get(v), d = rd[k].get(v), dwv = d * rw[k].get(v);
-        const float sig = sigmoid_v(zv), gate = zv * sig, slope = sig * fmaf(zv, 1.f - sig, 1.f);
-        const float x = FIRST ? yv * gate : yv;
-        const float dx = fmaf(-m, x, inv * (FIRST ? dwv : dwv * gate));
-        gy[v] = FIRST ? dx * gate : dx;
-        gz[v] = FIRST ? dx * yv * slope : dwv * (yv * inv) * slope;
-        dw[k][v] = live ? fmaf(FIRST ? d : d * gate, x * inv, dw[k][v]) : dw[k][v];
+        float more = dw[k][v];
+        norm_out_slopes<FIRST>(rz[k].get(v), ry[k].get(v), rd[k].get(v), rw[k].get(v), inv, m, gy[v], gz[v], more);
+        dw[k][v] = live ? more : dw[k][v];
       }
       if (live && seat.is(k))
         either(q.nt_out, [&](auto nt) {
@@ -484,37 +440,274 @@ __global__ __launch_bounds__(R::NT) void k_norm_out_bwd(
   store_part<R>(seat, q, dw, part + seat.part * E + e0);
 }
 
-// ---- launches ----
+// ---- long rows ----
 
-// calls f(R) with the row shape for `heads` heads of `width` channels: 8 channels
-// a thread (4 in rows of up to 256, 16 beyond 8192, 32 beyond 16384), so that a
-// row with its weights and their gradients leaves room for 16 waves a CU and
-// more.  Single channels where heads have fewer than 4, or so few more than 4
-// that the pieces of a row outnumber the largest shape's.
-static int64_t row_pieces(int64_t heads, int64_t width) {
-  const int64_t wide = heads * ((width + 3) / 4);
-  return width < 4 || wide > 8192 ? 0 : wide;
+constexpr int LT = 1024;  // threads along a row
+
+// the sums of a and b over the workgroup of LT threads
+__device__ __forceinline__ void long_sums(float& a, float& b) {
+  row_sums<Row<4, LT, 1>>(a, b, 0);
+  __syncthreads();  // the slots are free for the next row
 }
 
+// A row per workgroup and turn, read twice (the second time from the L2).
+template <typename T, int V>
+__global__ __launch_bounds__(LT) void k_long_in(const float* __restrict__ r, const T* __restrict__ p,
+                                                const float* __restrict__ s, const float* __restrict__ w,
+                                                Geo q, float eps, float* __restrict__ r_out,
+                                                T* __restrict__ u) {
+  for (int64_t row = blockIdx.x; row < q.tokens; row += gridDim.x) {
+    const int64_t at = row * q.EG;
+    auto value = [&](const Piece& pc, float(&x)[V]) {
+      Raw<float, V> rr, rs;
+      Raw<T, V> rp;
+      rr.load(element(r + at, pc.at));
+      if (p) rp.load(element(p + at, pc.at));
+      if (s) rs.load(element(s, pc.at));
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        x[v] = rr.get(v);
+        if (p) x[v] = s ? fmaf(rs.get(v), rp.get(v), x[v]) : x[v] + rp.get(v);
+      }
+    };
+    float sum = 0.f, none = 0.f;
+    for (int i = threadIdx.x; i < q.pieces; i += LT) {
+      const Piece pc = piece_of<V>(i, q);
+      float x[V];
+      value(pc, x);
+#pragma unroll
+      for (int v = 0; v < V; ++v) sum = v >= pc.skip ? fmaf(x[v], x[v], sum) : sum;
+      if (p) store_row<V>(element(r_out + at, pc.at), x);
+    }
+    long_sums(sum, none);
+    const float inv = inv_rms(sum, 1.f / (float)q.EG, eps);
+    for (int i = threadIdx.x; i < q.pieces; i += LT) {
+      const Piece pc = piece_of<V>(i, q);
+      float x[V];
+      Raw<float, V> rw;
+      value(pc, x);
+      rw.load(element(w, pc.at));
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = x[v] * inv * rw.get(v);
+      store_row<V>(element(u + at, pc.at), x);
+    }
+  }
+}
+
+// k and k^3 mean(c r) of every row
+template <typename T, int V>
+__global__ __launch_bounds__(LT) void k_long_in_means(const T* __restrict__ du, const float* __restrict__ r,
+                                                      const float* __restrict__ w, Geo q, float eps,
+                                                      float2* __restrict__ means) {
+  const float inv_n = 1.f / (float)q.EG;
+  for (int64_t row = blockIdx.x; row < q.tokens; row += gridDim.x) {
+    const int64_t at = row * q.EG;
+    float sq = 0.f, cr = 0.f;
+    for (int i = threadIdx.x; i < q.pieces; i += LT) {
+      const Piece pc = piece_of<V>(i, q);
+      Raw<float, V> rr, rw;
+      Raw<T, V> rd;
+      rr.load(element(r + at, pc.at));
+      rd.load(element(du + at, pc.at));
+      rw.load(element(w, pc.at));
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float y = rr.get(v), c = rd.get(v) * rw.get(v);
+        sq = v >= pc.skip ? fmaf(y, y, sq) : sq;
+        cr = v >= pc.skip ? fmaf(c, y, cr) : cr;
+      }
+    }
+    long_sums(sq, cr);
+    const float inv = inv_rms(sq, inv_n, eps);
+    if (threadIdx.x == 0) means[row] = make_float2(inv, inv * inv * inv * (cr * inv_n));
+  }
+}
+
+// a thread per piece, down the rows part, part + parts, ..
+template <typename T, int V>
+__global__ __launch_bounds__(256) void k_long_in_bwd(
+    const T* __restrict__ du, const float* __restrict__ dr_out, const float* __restrict__ r,
+    const T* __restrict__ p, const float* __restrict__ s, const float* __restrict__ w,
+    const float2* __restrict__ means, Geo q, float* __restrict__ dr, float* __restrict__ dp,
+    float* __restrict__ part) {
+  const Piece pc = piece_of<V>(blockIdx.x * 256 + threadIdx.x, q);
+  if (pc.skip == V) return;
+  Raw<float, V> rw, rs;
+  float dw[V], ds[V];
+  rw.load(element(w, pc.at));
+  if (s) rs.load(element(s, pc.at));
+#pragma unroll
+  for (int v = 0; v < V; ++v) dw[v] = ds[v] = 0.f;
+  for (int64_t row = blockIdx.y; row < q.tokens; row += q.parts) {
+    const int64_t at = row * q.EG;
+    Raw<float, V> rr, ro;
+    Raw<T, V> rd, rp;
+    rr.load(element(r + at, pc.at));
+    rd.load(element(du + at, pc.at));
+    if (dr_out) ro.load(element(dr_out + at, pc.at));
+    if (s) rp.load(element(p + at, pc.at));
+    const float2 mean = means[row];
+    float g[V], h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float y = rr.get(v), d = rd.get(v);
+      g[v] = fmaf(-mean.y, y, mean.x * (d * rw.get(v)));
+      if (dr_out) g[v] += ro.get(v);
+      dw[v] = fmaf(d, y * mean.x, dw[v]);
+      if (s) {
+        h[v] = rs.get(v) * g[v];
+        ds[v] = fmaf(g[v], rp.get(v), ds[v]);
+      }
+    }
+    store_row<V>(element(dr + at, pc.at), g);
+    if (s) store_row<V>(element(dp + at, pc.at), h);
+  }
+  store_row<V>(element(part + (int64_t)blockIdx.y * q.EG, pc.at), dw);
+  if (s) store_row<V>(element(part + (int64_t)(q.parts + blockIdx.y) * q.EG, pc.at), ds);
+}
+
+// Rows of norm out: unit = token x group.
+template <typename T, int V, bool FIRST>
+__global__ __launch_bounds__(LT) void k_long_out(const float* __restrict__ y, const T* __restrict__ z,
+                                                 const float* __restrict__ w, Geo q, Heads hd, float eps,
+                                                 T* __restrict__ o) {
+  const int64_t E = (int64_t)q.groups * q.EG, units = q.tokens * q.groups;
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int64_t token = unit / q.groups, e0 = (unit - token * q.groups) * q.EG, h0 = e0 / q.width;
+    const int64_t base = hd.base(token), at = token * E + e0;
+    auto value = [&](const Piece& pc, float(&x)[V], float(&n)[V]) {
+      Raw<float, V> ry;
+      Raw<T, V> rz;
+      ry.load(y + base + ((h0 + pc.head) * hd.N * hd.DH + ((int)pc.at - pc.head * q.width)));
+      rz.load(element(z + at, pc.at));
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float zv = rz.get(v);
+        x[v] = ry.get(v) * (zv * sigmoid_v(zv));
+        n[v] = FIRST ? x[v] : ry.get(v);
+      }
+    };
+    float sum = 0.f, none = 0.f;
+    for (int i = threadIdx.x; i < q.pieces; i += LT) {
+      const Piece pc = piece_of<V>(i, q);
+      float x[V], n[V];
+      value(pc, x, n);
+#pragma unroll
+      for (int v = 0; v < V; ++v) sum = v >= pc.skip ? fmaf(n[v], n[v], sum) : sum;
+    }
+    long_sums(sum, none);
+    const float inv = inv_rms(sum, 1.f / (float)q.EG, eps);
+    for (int i = threadIdx.x; i < q.pieces; i += LT) {
+      const Piece pc = piece_of<V>(i, q);
+      float x[V], n[V];
+      Raw<float, V> rw;
+      value(pc, x, n);
+      rw.load(element(w + e0, pc.at));
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = x[v] * inv * rw.get(v);
+      store_row<V>(element(o + at, pc.at), x);
+    }
+  }
+}
+
+template <typename T, int V, bool FIRST>
+__global__ __launch_bounds__(LT) void k_long_out_means(const T* __restrict__ d_out, const float* __restrict__ y,
+                                                       const T* __restrict__ z, const float* __restrict__ w,
+                                                       Geo q, Heads hd, float eps, float2* __restrict__ means) {
+  const int64_t E = (int64_t)q.groups * q.EG, units = q.tokens * q.groups;
+  const float inv_n = 1.f / (float)q.EG;
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int64_t token = unit / q.groups, e0 = (unit - token * q.groups) * q.EG, h0 = e0 / q.width;
+    const int64_t base = hd.base(token), at = token * E + e0;
+    float sq = 0.f, ct = 0.f;
+    for (int i = threadIdx.x; i < q.pieces; i += LT) {
+      const Piece pc = piece_of<V>(i, q);
+      Raw<float, V> ry, rw;
+      Raw<T, V> rz, rd;
+      ry.load(y + base + ((h0 + pc.head) * hd.N * hd.DH + ((int)pc.at - pc.head * q.width)));
+      rz.load(element(z + at, pc.at));
+      rd.load(element(d_out + at, pc.at));
+      rw.load(element(w + e0, pc.at));
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float zv = rz.get(v), gate = zv * sigmoid_v(zv);
+        const float x = FIRST ? ry.get(v) * gate : ry.get(v);
+        const float c = rd.get(v) * rw.get(v) * (FIRST ? 1.f : gate);
+        sq = v >= pc.skip ? fmaf(x, x, sq) : sq;
+        ct = v >= pc.skip ? fmaf(c, x, ct) : ct;
+      }
+    }
+    long_sums(sq, ct);
+    const float inv = inv_rms(sq, inv_n, eps);
+    if (threadIdx.x == 0) means[unit] = make_float2(inv, inv * inv * inv * (ct * inv_n));
+  }
+}
+
+// a thread per piece of a group, down the tokens part, part + parts, ..
+template <typename T, int V, bool FIRST>
+__global__ __launch_bounds__(256) void k_long_out_bwd(
+    const T* __restrict__ d_out, const float* __restrict__ y, const T* __restrict__ z,
+    const float* __restrict__ w, const float2* __restrict__ means, Geo q, Heads hd,
+    float* __restrict__ dy, float* __restrict__ dz, float* __restrict__ part) {
+  const int g = blockIdx.x / q.blocks;
+  const Piece pc = piece_of<V>((blockIdx.x - g * q.blocks) * 256 + threadIdx.x, q);
+  if (pc.skip == V) return;
+  const int64_t E = (int64_t)q.groups * q.EG, e0 = (int64_t)g * q.EG, h0 = e0 / q.width;
+  const int64_t off = (h0 + pc.head) * hd.N * hd.DH + ((int)pc.at - pc.head * q.width);
+  Raw<float, V> rw;
+  float dw[V];
+  rw.load(element(w + e0, pc.at));
+#pragma unroll
+  for (int v = 0; v < V; ++v) dw[v] = 0.f;
+  for (int64_t token = blockIdx.y; token < q.tokens; token += q.parts) {
+    const int64_t base = hd.base(token), at = token * E + e0;
+    Raw<float, V> ry;
+    Raw<T, V> rz, rd;
+    ry.load(y + base + off);
+    rz.load(element(z + at, pc.at));
+    rd.load(element(d_out + at, pc.at));
+    const float2 mean = means[token * q.groups + g];
+    float gy[V], gz[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      norm_out_slopes<FIRST>(rz.get(v), ry.get(v), rd.get(v), rw.get(v), mean.x, mean.y, gy[v], gz[v], dw[v]);
+    store_row<V>(dy + base + off, gy);
+    store_row<V>(element(dz + at, pc.at), gz);
+  }
+  store_row<V>(element(part + (int64_t)blockIdx.y * E + e0, pc.at), dw);
+}
+
+// ---- launches ----
+
+// Pieces of a group's row: of 4 channels, or of one where heads have fewer than 4.
+static int64_t row_pieces(int64_t heads, int64_t width) {
+  return width < 4 ? heads * width : heads * ((width + 3) / 4);
+}
+
+// Rows that do not fit a workgroup's registers, 8 channels a thread (512 channels
+// of such narrow heads).
+static bool is_long(int64_t heads, int64_t width) {
+  return row_pieces(heads, width) > (width < 4 ? 512 : 2048);
+}
+
+// calls f(R) with the row shape for `heads` heads of `width` channels: 8 channels
+// a thread (4 in rows of up to 256), so that a row with its weights and their
+// gradients leaves room for 16 waves a CU and more.
 template <typename F>
 static auto by_row(int64_t heads, int64_t width, F&& f) {
-  const int64_t n = row_pieces(heads, width), EG = heads * width;
-  if (n) {
-    if (n <= 16) return f(Row<4, 16, 1>{});
-    if (n <= 32) return f(Row<4, 32, 1>{});
-    if (n <= 64) return f(Row<4, 64, 1>{});
-    if (n <= 128) return f(Row<4, 64, 2>{});
-    if (n <= 256) return f(Row<4, 128, 2>{});
-    if (n <= 512) return f(Row<4, 256, 2>{});
-    if (n <= 1024) return f(Row<4, 512, 2>{});
-    if (n <= 2048) return f(Row<4, 1024, 2>{});
-    if (n <= 4096) return f(Row<4, 1024, 4>{});
-    return f(Row<4, 1024, 8>{});
+  const int64_t n = row_pieces(heads, width);
+  if (width < 4) {
+    if (n <= 64) return f(Row<1, 16, 4>{});
+    return f(Row<1, 64, 8>{});
   }
-  if (EG <= 64) return f(Row<1, 16, 4>{});
-  if (EG <= 512) return f(Row<1, 64, 8>{});
-  if (EG <= 8192) return f(Row<1, 1024, 8>{});
-  return f(Row<1, 1024, 32>{});
+  if (n <= 16) return f(Row<4, 16, 1>{});
+  if (n <= 32) return f(Row<4, 32, 1>{});
+  if (n <= 64) return f(Row<4, 64, 1>{});
+  if (n <= 128) return f(Row<4, 64, 2>{});
+  if (n <= 256) return f(Row<4, 128, 2>{});
+  if (n <= 512) return f(Row<4, 256, 2>{});
+  if (n <= 1024) return f(Row<4, 512, 2>{});
+  return f(Row<4, 1024, 2>{});
 }
 
 // Workgroups: enough to fill the 256 CUs with 2048 threads each (backwards with
@@ -535,7 +728,7 @@ static Geo geo_of(R, int64_t tokens, int64_t groups, int64_t heads, int64_t widt
   q.groups = (int)groups;
   q.EG = (int)(heads * width);
   q.width = (int)width;
-  q.pieces = (int)(R::V == 4 ? row_pieces(heads, width) : heads * width);
+  q.pieces = (int)row_pieces(heads, width);
   q.gpw = groups < R::SLOTS ? (int)groups : R::SLOTS;
   q.tpw = R::SLOTS / q.gpw;
   q.blocks = (int)((groups + q.gpw - 1) / q.gpw);
@@ -550,6 +743,31 @@ static Geo geo_by(int64_t tokens, int64_t groups, int64_t heads, int64_t width, 
                   int64_t bytes) {
   return by_row(heads, width,
                 [&](auto row) { return geo_of(row, tokens, groups, heads, width, backward, bytes); });
+}
+
+// Long rows: the rows' grid, and the backward's blocks of 256 pieces x parts of
+// the tokens (some 2048 workgroups); its workspace has the means behind the parts.
+static Geo long_geo(int64_t tokens, int64_t groups, int64_t heads, int64_t width) {
+  Geo q{};
+  q.tokens = tokens;
+  q.groups = (int)groups;
+  q.EG = (int)(heads * width);
+  q.width = (int)width;
+  q.pieces = (int)row_pieces(heads, width);
+  q.blocks = (q.pieces + 255) / 256;
+  const int64_t want = 2048 / (q.blocks * groups) + 1;
+  q.parts = (int)(tokens < want ? tokens : want);
+  return q;
+}
+
+static unsigned long_grid(int64_t rows) { return (unsigned)(rows < 1024 ? rows : 1024); }
+
+// calls f(T, V)
+template <typename F>
+static hipError_t by_long(bool bf16, int64_t width, F&& f) {
+  if (width < 4)
+    return bf16 ? f(uint16_t{}, std::integral_constant<int, 1>{}) : f(float{}, std::integral_constant<int, 1>{});
+  return bf16 ? f(uint16_t{}, std::integral_constant<int, 4>{}) : f(float{}, std::integral_constant<int, 4>{});
 }
 
 static hipError_t launch_sum_parts(const float* part, int n, int64_t E, float* out0, float* out1,
@@ -569,6 +787,13 @@ hipError_t launch_norm_in(bool bf16, const float* r, const void* p, const float*
                           int64_t rows, int64_t E, float eps, float* r_out, void* u,
                           hipStream_t stream) {
   const int64_t size = bf16 ? 2 : 4;
+  if (is_long(1, E))
+    return by_long(bf16, E, [&](auto t, auto v) {
+      using T = decltype(t);
+      hipLaunchKernelGGL((k_long_in<T, v.value>), dim3(long_grid(rows)), dim3(LT), 0, stream, r, (const T*)p, s, w,
+                         long_geo(rows, 1, 1, E), eps, r_out, (T*)u);
+      return hipGetLastError();
+    });
   return by_call(bf16, 1, E, [&](auto t, auto row) {
     using T = decltype(t);
     using R = decltype(row);
@@ -580,6 +805,7 @@ hipError_t launch_norm_in(bool bf16, const float* r, const void* p, const float*
 }
 
 size_t norm_in_backward_floats(int64_t rows, int64_t E) {
+  if (is_long(1, E)) return (size_t)(2 * long_geo(rows, 1, 1, E).parts * ((E + 1) / 2 * 2) + 2 * rows);
   return (size_t)(2 * geo_by(rows, 1, 1, E, true, 0).parts * E);
 }
 
@@ -587,15 +813,32 @@ hipError_t launch_norm_in_backward(bool bf16, const void* du, const float* dr_ou
                                    const void* p, const float* s, const float* w, int64_t rows,
                                    int64_t E, float eps, float* dr, float* dp, float* dw, float* ds,
                                    float* ws, hipStream_t stream) {
+  if (rows && is_long(1, E)) {
+    const Geo q = long_geo(rows, 1, 1, E);
+    float2* means = (float2*)(ws + 2 * q.parts * ((E + 1) / 2 * 2));
+    const hipError_t e = by_long(bf16, E, [&](auto t, auto v) {
+      using T = decltype(t);
+      hipLaunchKernelGGL((k_long_in_means<T, v.value>), dim3(long_grid(rows)), dim3(LT), 0, stream, (const T*)du,
+                         r, w, q, eps, means);
+      hipLaunchKernelGGL((k_long_in_bwd<T, v.value>), dim3((unsigned)q.blocks, (unsigned)q.parts), dim3(256), 0,
+                         stream, (const T*)du, dr_out, r, (const T*)p, s, w, means, q, dr, dp, ws);
+      return hipGetLastError();
+    });
+    return e != hipSuccess ? e : launch_sum_parts(ws, q.parts, E, dw, ds, stream);
+  }
   const int64_t size = bf16 ? 2 : 4;
   const Geo q = geo_by(rows, 1, 1, E, true, rows * E * (8 + size + (dr_out ? 4 : 0) + (s ? 4 + size : 0)));
   if (rows) {
     const hipError_t e = by_call(bf16, 1, E, [&](auto t, auto row) {
       using T = decltype(t);
       using R = decltype(row);
-      hipLaunchKernelGGL((k_norm_in_bwd<T, R>), dim3((unsigned)q.parts), dim3(R::NT), 0, stream,
-                         (const T*)du, dr_out, r, (const T*)p, s, w, q, eps, dr, dp, ws);
-      return hipGetLastError();
+      auto go = [&](auto scaled, auto added) {
+        hipLaunchKernelGGL((k_norm_in_bwd<T, R, scaled.value, added.value>), dim3((unsigned)q.parts),
+                           dim3(R::NT), 0, stream, (const T*)du, dr_out, r, (const T*)p, s, w, q, eps, dr, dp, ws);
+        return hipGetLastError();
+      };
+      if (s) return dr_out ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+      return dr_out ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
     });
     if (e != hipSuccess) return e;
   }
@@ -605,6 +848,17 @@ hipError_t launch_norm_in_backward(bool bf16, const void* du, const float* dr_ou
 hipError_t launch_norm_out(bool bf16, bool gate_first, const float* y, const void* z,
                            const float* w, int64_t B, int64_t H, int64_t N, int64_t DH,
                            int64_t groups, float eps, void* o, hipStream_t stream) {
+  if (is_long(H / groups, DH))
+    return by_long(bf16, DH, [&](auto t, auto v) {
+      using T = decltype(t);
+      auto go = [&](auto first) {
+        hipLaunchKernelGGL((k_long_out<T, v.value, first.value>), dim3(long_grid(B * N * groups)), dim3(LT), 0,
+                           stream, y, (const T*)z, w, long_geo(B * N, groups, H / groups, DH), Heads{H, N, DH}, eps,
+                           (T*)o);
+        return hipGetLastError();
+      };
+      return gate_first ? go(std::true_type{}) : go(std::false_type{});
+    });
   return by_call(bf16, H / groups, DH, [&](auto t, auto row) {
     using T = decltype(t);
     using R = decltype(row);
@@ -619,6 +873,8 @@ hipError_t launch_norm_out(bool bf16, bool gate_first, const float* y, const voi
 }
 
 size_t norm_out_backward_floats(int64_t B, int64_t H, int64_t N, int64_t DH, int64_t groups) {
+  if (is_long(H / groups, DH))
+    return (size_t)(long_geo(B * N, groups, H / groups, DH).parts * ((H * DH + 1) / 2 * 2) + 2 * B * N * groups);
   return (size_t)(geo_by(B * N, groups, H / groups, DH, true, 0).parts * H * DH);
 }
 
@@ -627,6 +883,23 @@ hipError_t launch_norm_out_backward(bool bf16, bool gate_first, const void* d_ou
                                     int64_t DH, int64_t groups, float eps, float* dy, float* dz,
                                     float* dw, float* ws, hipStream_t stream) {
   const int64_t tokens = B * N;
+  if (tokens && is_long(H / groups, DH)) {
+    const Geo q = long_geo(tokens, groups, H / groups, DH);
+    float2* means = (float2*)(ws + q.parts * ((H * DH + 1) / 2 * 2));
+    const hipError_t e = by_long(bf16, DH, [&](auto t, auto v) {
+      using T = decltype(t);
+      auto go = [&](auto first) {
+        hipLaunchKernelGGL((k_long_out_means<T, v.value, first.value>), dim3(long_grid(tokens * groups)), dim3(LT),
+                           0, stream, (const T*)d_out, y, (const T*)z, w, q, Heads{H, N, DH}, eps, means);
+        hipLaunchKernelGGL((k_long_out_bwd<T, v.value, first.value>),
+                           dim3((unsigned)(q.blocks * groups), (unsigned)q.parts), dim3(256), 0, stream,
+                           (const T*)d_out, y, (const T*)z, w, means, q, Heads{H, N, DH}, dy, dz, ws);
+        return hipGetLastError();
+      };
+      return gate_first ? go(std::true_type{}) : go(std::false_type{});
+    });
+    return e != hipSuccess ? e : launch_sum_parts(ws, q.parts, H * DH, dw, nullptr, stream);
+  }
   const Geo q = geo_by(tokens, groups, H / groups, DH, true, tokens * H * DH * (bf16 ? 16 : 20));
   if (tokens) {
     const hipError_t e = by_call(bf16, H / groups, DH, [&](auto t, auto row) {

@@ -309,7 +309,7 @@ NORM_IN = [(1, 1, "f32"), (3, 7, "bf16"), (5, 64, "f32"), (70, 33, "bf16"), (9, 
            (33, 1024, "bf16"), (2, 1025, "bf16"), (6, 2048, "bf16"), (300, 260, "f32"), (3, 4096, "f32"),
            (2, 5001, "bf16"), (2, 16384, "bf16"), (1, 20000, "f32"), (2, 32768, "bf16"), (1, 32767, "f32"),
            (2500, 64, "bf16"), (5000, 36, "f32"),
-           (7, 5, "f32"), (7, 6, "bf16"), (40, 129, "f32"), (3, 9001, "bf16"), (2, 2, "bf16")]
+           (7, 5, "f32"), (7, 6, "bf16"), (40, 129, "f32"), (3, 9001, "bf16"), (2, 2, "bf16"), (1100, 8200, "f32")]
 
 
 @pytest.mark.parametrize("R,E,dtype", NORM_IN)
@@ -364,7 +364,7 @@ NORM_OUT = [(1, 1, 1, 1, 1, "f32"), (2, 3, 5, 7, 1, "bf16"), (2, 3, 5, 7, 3, "f3
             (1, 1, 700, 64, 1, "bf16"), (1, 512, 2, 64, 1, "bf16"), (1, 7, 2, 4681, 1, "f32"), (130, 2, 20, 32, 2, "f32"),
             (1, 1, 3000, 4, 1, "bf16"), (2, 600, 2, 64, 2, "f32"),
             (2, 9, 7, 5, 1, "bf16"), (2, 9, 7, 6, 9, "f32"), (3, 8, 40, 33, 2, "bf16"), (2, 5, 3, 3, 1, "bf16"), (1, 500, 3, 2, 1, "f32"),
-            (1, 6553, 1, 5, 1, "bf16"), (2, 8, 9, 128, 8, "bf16"), (1, 64, 2, 127, 2, "f32")]
+            (1, 6553, 1, 5, 1, "bf16"), (2, 8, 9, 128, 8, "bf16"), (1, 64, 2, 127, 2, "f32"), (2, 300, 5, 63, 2, "bf16"), (1, 1200, 3, 3, 2, "bf16")]
 
 
 def norm_out_inputs(B, H, N, d, dtype, seed):

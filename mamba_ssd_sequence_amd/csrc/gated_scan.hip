@@ -173,7 +173,7 @@ __device__ __forceinline__ float join_tiles(Joint<TL>& j, int wave, int c, bool 
   words += c;
   float P = 1.f, U = 0.f;
   if (wave == 0 && exists && tiles > 1) {
-#pragma unroll 4
+#pragma unroll
     for (int i = 0; i < NW; ++i) {
       U = fmaf(j.P[slot(i)], U, j.U[slot(i)]);
       P *= j.P[slot(i)];
@@ -215,11 +215,11 @@ __device__ __forceinline__ float join_tiles(Joint<TL>& j, int wave, int c, bool 
       h = low_value(s);
     }
     if (order > start)
-#pragma unroll 4
+#pragma unroll
       for (int i = 0; i < NW; ++i) h = fmaf(j.spanP[i * C + c], h, j.spanU[i * C + c]);
     if (order % SPAN == SPAN - 1 && order + 1 < tiles)
       put_word(states + ((int64_t)span + 1) * C, MARK, fmaf(P, h, U));
-#pragma unroll 4
+#pragma unroll
     for (int i = 0; i < NW; ++i) {
       j.H[slot(i)] = h;
       h = fmaf(j.P[slot(i)], h, j.U[slot(i)]);
@@ -455,16 +455,38 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
 
 // ---- single tokens ----
 
+// 4 channels a thread, the last n % 4 by one thread one by one (a piece moved
+// back to the end would read channels that the step in place has written).
+template <typename T, int SCALE, int V>
+__device__ __forceinline__ void step_piece(const T* x, const T* A, const T* I, const float* state, int64_t i,
+                                           float* out) {
+  Raw<T, V> rx, rA, rI;
+  Raw<float, V> rh;
+  rA.load(A + i);
+  if (I) rI.load(I + i);
+  rx.load(x + i);
+  rh.load(state + i);
+  float h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float a, beta;
+    decay_of<SCALE>(rA.get(v), a, beta);
+    const float g = I ? sigmoid_v(rI.get(v)) : 1.f;
+    h[v] = fmaf(a, rh.get(v), beta * g * rx.get(v));
+  }
+  store_row<V>(out + i, h);
+}
+
 template <typename T, int SCALE>
 __global__ __launch_bounds__(256) void k_gated_step(const T* __restrict__ x, const T* __restrict__ A,
                                                     const T* __restrict__ I, const float* state,
                                                     int64_t n, float* out) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  float a, beta;
-  decay_of<SCALE>(Elem<T>::ld(A, i), a, beta);
-  const float g = I ? sigmoid_v(Elem<T>::ld(I, i)) : 1.f;
-  out[i] = fmaf(a, state[i], beta * g * Elem<T>::ld(x, i));
+  int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i + 4 <= n) {
+    step_piece<T, SCALE, 4>(x, A, I, state, i, out);
+  } else {
+    for (; i < n; ++i) step_piece<T, SCALE, 1>(x, A, I, state, i, out);
+  }
 }
 
 // calls f<T, SCALE>()
@@ -598,7 +620,7 @@ hipError_t launch_gated_scan_step(bool bf16, int scale, const void* x, const voi
                                   hipStream_t stream) {
   return by_type(bf16, scale, [&](auto t, auto sc) {
     using T = decltype(t);
-    hipLaunchKernelGGL((k_gated_step<T, sc.value>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0,
+    hipLaunchKernelGGL((k_gated_step<T, sc.value>), dim3((unsigned)((n + 1023) / 1024)), dim3(256), 0,
                        stream, (const T*)x, (const T*)A, (const T*)I, state, n, out);
     return hipGetLastError();
   });

@@ -584,14 +584,15 @@ def gated_scan_backward(x, A_proj, I_proj, y, dy, *, scale: int, initial_state=N
     i, f32, xt, shape = dev.index, torch.float32, x.dtype, x.shape
     B, H, N, d_h = shape
     state = (B, H, d_h)
-    dx = torch.empty(shape, dtype=f32, device=dev)
-    dA = torch.empty(shape, dtype=f32, device=dev)
-    dI = torch.empty(shape, dtype=f32, device=dev) if I_proj is not None else None
-    dh0 = torch.empty(state, dtype=f32, device=dev) if initial_state is not None else None
+    py, ph0 = _at(y, "y", f32, shape, i, dev), _at(initial_state, "initial_state", f32, state, i, dev)
+    if y is None:
+        raise TypeError("y must be a torch.Tensor")
+    dx, dA = torch.empty_like(y), torch.empty_like(y)
+    dI = torch.empty_like(y) if I_proj is not None else None
+    dh0 = torch.empty_like(initial_state) if initial_state is not None else None
     ws, nbytes, keep = _scratch(workspace, _scratch_size("ssd_gated_scan_backward_workspace_size", B, H, N, d_h), dev)
     _call(lib().ssd_gated_scan_backward, i, x.data_ptr(), _at(A_proj, "A_proj", xt, shape, i, dev),
-          _at(I_proj, "I_proj", xt, shape, i, dev), _at(initial_state, "initial_state", f32, state, i, dev),
-          _at(y, "y", f32, shape, i, dev), _at(dy, "dy", f32, shape, i, dev),
+          _at(I_proj, "I_proj", xt, shape, i, dev), ph0, py, _at(dy, "dy", f32, shape, i, dev),
           _at(d_final_state, "d_final_state", f32, state, i, dev), B, H, N, d_h, scale, kind, dx.data_ptr(),
           dA.data_ptr(), dI.data_ptr() if dI is not None else None, dh0.data_ptr() if dh0 is not None else None,
           ws, nbytes)
@@ -610,9 +611,9 @@ def norm_in(residual, branch, branch_scale, weight, eps: float, *, dtype=None, r
     if branch is not None:
         dtype = branch.dtype
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=f32, device=dev)
+            residual_out = torch.empty_like(residual)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+        out = torch.empty_like(residual, dtype=dtype)
     kind, dtype = _qkv_dtype(out), (out.dtype if dtype is None else dtype)
     rows = residual.numel() // E if E else 0
     _call(lib().ssd_norm_in, i, residual.data_ptr(), _at(branch, "branch", dtype, shape, i, dev),
@@ -636,15 +637,17 @@ def norm_in_backward(d_out, d_residual_out, residual_out, branch, branch_scale, 
     if branch_scale is None:
         branch = None
     rows = d_out.numel() // E if E else 0
-    d_residual = torch.empty(shape, dtype=f32, device=dev)
-    d_weight = torch.empty((E,), dtype=f32, device=dev)
-    d_branch = torch.empty(shape, dtype=f32, device=dev) if branch is not None else None
-    d_scale = torch.empty((E,), dtype=f32, device=dev) if branch is not None else None
+    pr, pw = _at(residual_out, "residual_out", f32, shape, i, dev), _at(weight, "weight", f32, (E,), i, dev)
+    if residual_out is None or weight is None:
+        raise TypeError("residual_out and weight must be torch.Tensors")
+    d_residual, d_weight = torch.empty_like(residual_out), torch.empty_like(weight)
+    d_branch = torch.empty_like(residual_out) if branch is not None else None
+    d_scale = torch.empty_like(weight) if branch is not None else None
     ws, nbytes, keep = _scratch(workspace, _scratch_size("ssd_norm_in_backward_workspace_size", rows, E), dev)
     _call(lib().ssd_norm_in_backward, i, d_out.data_ptr(),
-          _at(d_residual_out, "d_residual_out", f32, shape, i, dev), _at(residual_out, "residual_out", f32, shape, i, dev),
+          _at(d_residual_out, "d_residual_out", f32, shape, i, dev), pr,
           _at(branch, "branch", d_out.dtype, shape, i, dev), _at(branch_scale, "branch_scale", f32, (E,), i, dev),
-          _at(weight, "weight", f32, (E,), i, dev), rows, E, eps, kind, d_residual.data_ptr(),
+          pw, rows, E, eps, kind, d_residual.data_ptr(),
           d_branch.data_ptr() if branch is not None else None, d_weight.data_ptr(),
           d_scale.data_ptr() if branch is not None else None, ws, nbytes)
     return d_residual, (d_residual if d_branch is None else d_branch), d_weight, d_scale
@@ -660,7 +663,7 @@ def norm_out(y, z, weight, eps: float, *, groups: int = 1, gate_first: bool = Tr
     B, H, N, d_h = y.shape
     shape = (B, N, H * d_h)
     if out is None:
-        out = torch.empty(shape, dtype=zt, device=dev)
+        out = torch.empty_like(z)
     _call(lib().ssd_norm_out, i, y.data_ptr(), _at(z, "z", zt, shape, i, dev),
           _at(weight, "weight", torch.float32, (H * d_h,), i, dev), B, H, N, d_h, groups, 1 if gate_first else 0, eps,
           kind, _at(out, "out", zt, shape, i, dev))
@@ -677,12 +680,13 @@ def norm_out_backward(d_out, y, z, weight, eps: float, *, groups: int = 1, gate_
     _require(y, "y", f32, dev)
     B, H, N, d_h = y.shape
     shape = (B, N, H * d_h)
-    dy = torch.empty(y.shape, dtype=f32, device=dev)
-    dz = torch.empty(shape, dtype=f32, device=dev)
-    d_weight = torch.empty((H * d_h,), dtype=f32, device=dev)
+    pw = _at(weight, "weight", f32, (H * d_h,), i, dev)
+    if weight is None:
+        raise TypeError("weight must be a torch.Tensor")
+    dy, dz, d_weight = torch.empty_like(y), torch.empty_like(z, dtype=f32), torch.empty_like(weight)
     ws, nbytes, keep = _scratch(workspace,
                                 _scratch_size("ssd_norm_out_backward_workspace_size", B, H, N, d_h, groups), dev)
     _call(lib().ssd_norm_out_backward, i, _at(d_out, "d_out", zt, shape, i, dev), y.data_ptr(),
-          _at(z, "z", zt, shape, i, dev), _at(weight, "weight", f32, (H * d_h,), i, dev), B, H, N, d_h, groups,
+          _at(z, "z", zt, shape, i, dev), pw, B, H, N, d_h, groups,
           1 if gate_first else 0, eps, kind, dy.data_ptr(), dz.data_ptr(), d_weight.data_ptr(), ws, nbytes)
     return dy, dz, d_weight

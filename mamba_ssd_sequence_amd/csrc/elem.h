@@ -32,8 +32,8 @@ __device__ __forceinline__ float sigmoid_v(float x) {
   return __builtin_amdgcn_rcpf(1.f + exp_fast(-x));
 }
 
-// Nontemporal accesses (NT), for arrays that pass through once and are larger
-// than the last-level cache: they leave the caches to what is used again.
+// Nontemporal accesses (NT), for arrays that pass through once: they leave the
+// caches to what is used again.
 template <bool NT, typename P>
 __device__ __forceinline__ P load_as(const void* p) {
   const P* q = static_cast<const P*>(p);
@@ -71,9 +71,6 @@ __device__ __forceinline__ T* element(T* p, unsigned e) {
   typedef typename std::conditional<std::is_const<T>::value, const char, char>::type byte;
   return reinterpret_cast<T*>(reinterpret_cast<byte*>(p) + e * (unsigned)sizeof(T));
 }
-
-// The last-level cache.
-constexpr int64_t CACHE_BYTES = (int64_t)256 << 20;
 
 // Pieces of 4 elements, at the alignment of one: rows of any width are read and
 // written in whole pieces (the hardware takes them at any element's address).

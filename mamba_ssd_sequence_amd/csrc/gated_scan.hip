@@ -277,7 +277,7 @@ template <typename T, int SCALE, bool GATE, typename TL>
 __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan(
     const T* __restrict__ x, const T* __restrict__ A, const T* __restrict__ I,
     const float* __restrict__ h0, int64_t N, int DH, int width, int slabs, int heads, int tiles, int runs,
-    bool nt_in, bool nt_out, float* __restrict__ y, float* __restrict__ hf, unsigned* counters, word_t* words) {
+    bool nt_row, float* __restrict__ y, float* __restrict__ hf, unsigned* counters, word_t* words) {
   constexpr int V = TL::V, TT = TL::TT, C = TL::C;
   __shared__ Joint<TL> j;
   const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
@@ -296,7 +296,7 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan(
   float* yt = y + sp.base;
 
   Raw<T, V> rx[TT], rA[TT], rI[TT];
-  either(nt_in, [&](auto nt) {
+  either(nt_row, [&](auto nt) {
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
       const unsigned at = sp.at(i, DH);
@@ -338,7 +338,7 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan(
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], u[i][v]);
     if (sp.live && sp.tok + i < sp.rows) {
-      either(nt_out, [&](auto nt) { store_row<V, nt.value>(element(yt, sp.at(i, DH)), h); });
+      either(nt_row, [&](auto nt) { store_row<V, nt.value>(element(yt, sp.at(i, DH)), h); });
       if (last && sp.tok + i == sp.rows - 1) store_row<V>(hf + state + sp.c, h);
     }
   }
@@ -355,7 +355,7 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
     const T* __restrict__ x, const T* __restrict__ A, const T* __restrict__ I,
     const float* __restrict__ h0, const float* __restrict__ y, const float* __restrict__ dy,
     const float* __restrict__ dlast, int64_t N, int DH, int width, int slabs, int heads, int tiles, int runs,
-    bool nt_in, bool nt_out, float* __restrict__ dx, float* __restrict__ dA, float* __restrict__ dI,
+    bool nt_row, float* __restrict__ dx, float* __restrict__ dA, float* __restrict__ dI,
     float* __restrict__ dh0, unsigned* counters, word_t* words) {
   constexpr int V = TL::V, TT = TL::TT, C = TL::C;
   __shared__ Joint<TL> j;
@@ -378,7 +378,7 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
 
   Raw<T, V> rA[TT], rx[TT], rI[TT];
   Raw<float, V> rd[TT], rp[TT], r0;
-  either(nt_in, [&](auto nt) {
+  either(nt_row, [&](auto nt) {
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
       rA[i].template load<nt.value>(element(At, sp.at(i, DH)));
@@ -443,7 +443,7 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
       carry[v] = a * lam;
     }
     const unsigned at = sp.at(i, DH);
-    either(nt_out, [&](auto nt) {
+    either(nt_row, [&](auto nt) {
       store_row<V, nt.value>(element(dxt, at), ox);
       store_row<V, nt.value>(element(dAt, at), oA);
       if constexpr (GATE) store_row<V, nt.value>(element(dIt, at), oI);
@@ -554,21 +554,12 @@ size_t gated_scan_backward_floats(int64_t BH, int64_t N, int64_t DH) {
   return split_of(BH, N, DH, BWD_TOKENS).floats();
 }
 
-// The inputs pass through once: nontemporal loads (4 x 16 heads of 2048 tokens,
-// bf16, backwards: 44.6 us against 47.5) where rows are whole 128-byte lines of
-// fp32; else two rows share a line, which has to stay for the second (33
-// channels, backwards: 59.0 us against 34.7).  The outputs too, but for calls
-// that move between one and three times the last-level cache, which still takes
-// up much of what is written: stores nontemporal / not, 84 MB 19.1 / 20.1 us, 168
-// MB 37.2 / 40.5, 671 MB (32 x 16 heads) 129 / 113, 1007 MB 181 / 191; backwards 426
-// MB 92.7 / 79.7, 872 MB 171 / 178.
-struct Passing {
-  bool in, out;
-};
-static Passing passing(int64_t DH, int64_t bytes) {
-  const bool lines = DH % 32 == 0;
-  return {lines, lines && (bytes < CACHE_BYTES || bytes >= 3 * CACHE_BYTES)};
-}
+// Inputs and outputs pass through once: nontemporal accesses where rows are whole
+// 128-byte lines of fp32 (plain / nontemporal, bf16 with gate: 4 x 16 heads of 2048
+// tokens 19.3 / 18.4 us, 1 x 16 of 65536 144.5 / 129.8; backwards 58.0 / 45.3); else
+// two rows share a line, which has to stay for the second (33 channels,
+// backwards: 34.7 / 59.0).
+static bool passing(int64_t DH) { return DH % 32 == 0; }
 
 static hipError_t clear_words(const Split& s, float* ws, hipStream_t stream) {
   const int64_t n = (int64_t)((s.floats() + 3) / 4), want = (n + 255) / 256;
@@ -601,7 +592,6 @@ hipError_t launch_gated_scan(bool bf16, int scale, const void* x, const void* A,
                              const float* h0, int64_t BH, int64_t N, int64_t DH, float* y,
                              float* hf, float* ws, hipStream_t stream) {
   const Split s = split_of(BH, N, DH, fwd_tokens(bf16));
-  const Passing nt = passing(DH, BH * N * DH * ((I ? 3 : 2) * (bf16 ? 2 : 4) + 4));
   const hipError_t e = clear_words(s, ws, stream);
   if (e != hipSuccess) return e;
   return by_call(bf16, scale, I != nullptr, DH, s.waves, [&](auto t, auto sc, auto g, auto k, auto nw) {
@@ -609,7 +599,7 @@ hipError_t launch_gated_scan(bool bf16, int scale, const void* x, const void* A,
     using TL = Tile<kind_v(k.value), kind_lpr(k.value), nw.value, fwd_tokens(sizeof(T) == 2)>;
     hipLaunchKernelGGL((k_gated_scan<T, sc.value, g.value, TL>), dim3((unsigned)(s.heads * s.tiles)),
                        dim3(TL::NW * WAVE), 0, stream, (const T*)x, (const T*)A, (const T*)I, h0, N,
-                       (int)DH, s.width, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs, nt.in, nt.out, y, hf, (unsigned*)ws,
+                       (int)DH, s.width, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs, passing(DH), y, hf, (unsigned*)ws,
                        (word_t*)(ws + s.counters()));
     return hipGetLastError();
   });
@@ -632,7 +622,6 @@ hipError_t launch_gated_scan_backward(bool bf16, int scale, const void* x, const
                                       int64_t DH, float* dx, float* dA, float* dI, float* dh0,
                                       float* ws, hipStream_t stream) {
   const Split s = split_of(BH, N, DH, BWD_TOKENS);
-  const Passing nt = passing(DH, BH * N * DH * ((I ? 3 : 2) * (bf16 ? 6 : 8) + 8));
   const hipError_t e = clear_words(s, ws, stream);
   if (e != hipSuccess) return e;
   return by_call(bf16, scale, I != nullptr, DH, s.waves, [&](auto t, auto sc, auto g, auto k, auto nw) {
@@ -640,7 +629,7 @@ hipError_t launch_gated_scan_backward(bool bf16, int scale, const void* x, const
     using TL = Tile<kind_v(k.value), kind_lpr(k.value), nw.value, BWD_TOKENS>;
     hipLaunchKernelGGL((k_gated_scan_bwd<T, sc.value, g.value, TL>), dim3((unsigned)(s.heads * s.tiles)),
                        dim3(TL::NW * WAVE), 0, stream, (const T*)x, (const T*)A, (const T*)I, h0, y, dy,
-                       dlast, N, (int)DH, s.width, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs, nt.in, nt.out, dx, dA, dI, dh0,
+                       dlast, N, (int)DH, s.width, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs, passing(DH), dx, dA, dI, dh0,
                        (unsigned*)ws, (word_t*)(ws + s.counters()));
     return hipGetLastError();
   });

@@ -712,18 +712,18 @@ static auto by_row(int64_t heads, int64_t width, F&& f) {
 
 // Workgroups: enough to fill the 256 CUs with 2048 threads each (backwards with
 // 1024, whose sums then add up over fewer parts), no more than there is work for.
-// Nontemporal loads where a call moves more than the last-level cache (256 MB)
-// holds, nontemporal stores too where it moves 768 MB and more (below that the
-// cache still takes up much of what is written).  Norm in, E 1024 (plain / loads /
-// both): 101 MB 16.0 / 18.1 / 18.4 us, 403 MB 74.3 / 61.8 / 69.3, 805 MB 150 / 149
-// / 140; backwards 168 MB 33.1 / 33.4 / 35.0, 671 MB 129 / 108 / 118, 1342 MB 260 /
-// 259 / 233.
+// Nontemporal stores where a call moves 128 MB and more, half of the last-level
+// cache, loads too from 192 MB on; smaller calls find their arrays in the cache and
+// leave them there.  Plain / stores / loads / both: norm in, bf16, E 1024, 101 MB 16.0 /
+// 16.4 / 18.5 / 18.9 us, 403 MB 74.9 / 72.7 / 73.4 / 69.3; norm out backwards 134 MB
+// 31.3 / 27.0 / 31.1 / 30.5; norm in backwards 168 MB 37.0 / 34.7 / 34.6 / 35.2, 671 MB
+// 130 / 125 / 127 / 121, 1342 MB 258 / 249 / 256 / 243.
 template <typename R>
 static Geo geo_of(R, int64_t tokens, int64_t groups, int64_t heads, int64_t width, bool backward,
                   int64_t bytes) {
   Geo q{};
-  q.nt_in = bytes >= CACHE_BYTES;
-  q.nt_out = bytes >= 3 * CACHE_BYTES;
+  q.nt_in = bytes >= (int64_t)192 << 20;
+  q.nt_out = bytes >= (int64_t)128 << 20;
   q.tokens = tokens;
   q.groups = (int)groups;
   q.EG = (int)(heads * width);

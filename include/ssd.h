@@ -402,9 +402,14 @@ ssd_status ssd_prep_amask_backward(const float* A_proj, const float* dt_proj, co
  *
  * A_P = +inf gives a = 0 exactly: nothing from before the token is kept, which
  * starts a new sequence inside a row (gradients included).  A_P = -inf gives
- * a = 1 and beta = 0 (SSD_INPUT_PLAIN: 1): the state is kept.  A NaN or an
- * infinite x reaches the outputs of its channel from its token on, up to the
- * next such start or beyond it (0 inf = NaN, as in the recurrence itself).
+ * a = 1 and beta = 0 (SSD_INPUT_PLAIN: 1): the state is kept, which passes over
+ * padding.  Logits beyond -87 and 87 count as infinite (e^-87 is the smallest
+ * normal fp32 number).  A NaN or an infinite x reaches the outputs of its
+ * channel from its token on, also past a later start (0 inf = NaN, as in the
+ * recurrence itself), and no other channel.
+ *
+ * These calls, and the norms' below, launch on the current device, which has to
+ * be that of the arrays.
  *
  * SSD_INPUT_PLAIN:  beta = 1.
  * SSD_INPUT_CONVEX: beta = 1 - a, so that h is a weighted mean of what came in.
@@ -484,8 +489,10 @@ ssd_status ssd_gated_scan_backward(const void* x, const void* A_proj, const void
  * weight per channel, a SiLU gate and a residual scale per channel.
  * Outgoing gradients are f32, as ssd_backward's; an incoming gradient has the
  * type of its array.  eps >= 0; with eps = 0 a row of zeros gives NaN, as the
- * quotient does.  Sums of squares and gradient sums are fp32; the weight
- * gradients are summed over rows in a fixed order (deterministic).
+ * quotient does.  Sums of squares and gradient sums are fp32 (a row whose squares
+ * pass its range, values around 1e19, comes out as zeros); the weight gradients
+ * are summed over rows in a fixed order (deterministic).  A workspace serves one
+ * call at a time.
  *
  * ssd_norm_in -- what the previous block's output projection made is scaled
  * and added to the residual stream, whose RMS norm is the next block's input:

@@ -46,7 +46,7 @@ __device__ __forceinline__ void decay_slope(float A, float& a, float& rest, floa
 
 // ---- whole sequences ----
 //
-// One workgroup takes a tile: TILE consecutive tokens of C channels of one
+// One workgroup takes a tile: TOKENS consecutive tokens of C channels of one
 // head, read once, held in registers as decays and inputs, and written once.
 // Lane l of a wave owns V channels (l % LPR) of TT consecutive tokens (its
 // group l / LPR); groups, then waves, follow each other along the tokens.
@@ -59,7 +59,12 @@ __device__ __forceinline__ void decay_slope(float A, float& a, float& rest, floa
 //     the tile and each of its waves.
 //  3. Every thread runs its tokens from its own entering state and writes y.
 // The alternative, a pass over the inputs for the segments' steps and a second
-// one for the outputs, reads x, A_P and I_P twice.
+// one for the outputs, reads x, A_P and I_P twice.  Memory bounds both directions:
+// 1 x 16 heads of 65536 tokens x 64 channels, bf16 with gate, 671 MB that have to
+// move and 677 MB that the counters see, 129 us (5.2 TB/s; a copy of that size
+// makes 5.1); 4 x 16 heads of 2048 tokens 84 MB in 18.1 us (loading, joining and
+// storing do not overlap when every tile is resident at once), backwards 218 MB in
+// 46 us.  A tile's 39 instruction slots an element would take half of that.
 //
 // Waiting.  A workgroup takes the next tile of its head from a counter, so the
 // tiles before its own belong to workgroups that have started; each publishes
@@ -289,59 +294,59 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan(
   float enter = 0.f;  // in the first wave: the state entering the sequence, then each next tile
   if (wave == 0 && exists && h0) enter = h0[state + lane];
   for (int k = 0; k < runs; ++k) {
-  const int tile = taken + k;
-  asm("" : "+s"(DH));  // a tile's offsets are not worth registers over the loop
-  const Spot<TL> sp(bh, start, tile, N, DH, width);
-  const T *xt = x + sp.base, *At = A + sp.base, *It = I + sp.base;
-  float* yt = y + sp.base;
+    const int tile = taken + k;
+    asm("" : "+s"(DH));  // a tile's offsets are not worth registers over the loop
+    const Spot<TL> sp(bh, start, tile, N, DH, width);
+    const T *xt = x + sp.base, *At = A + sp.base, *It = I + sp.base;
+    float* yt = y + sp.base;
 
-  Raw<T, V> rx[TT], rA[TT], rI[TT];
-  either(nt_row, [&](auto nt) {
+    Raw<T, V> rx[TT], rA[TT], rI[TT];
+    either(nt_row, [&](auto nt) {
 #pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      const unsigned at = sp.at(i, DH);
-      rA[i].template load<nt.value>(element(At, at));
-      if constexpr (GATE) rI[i].template load<nt.value>(element(It, at));
-      rx[i].template load<nt.value>(element(xt, at));
-    }
-  });
-  float a[TT][V], u[TT][V], P[V], U[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    P[v] = 1.f;
-    U[v] = 0.f;
-  }
-#pragma unroll
-  for (int i = 0; i < TT; ++i) {
-    rA[i].or_else(sp.tok + i < sp.rows, 0xff80u);  // tokens past the end leave the state alone:
-    rx[i].or_else(sp.tok + i < sp.rows, 0u);       // A_P = -inf, x = 0
+      for (int i = 0; i < TT; ++i) {
+        const unsigned at = sp.at(i, DH);
+        rA[i].template load<nt.value>(element(At, at));
+        if constexpr (GATE) rI[i].template load<nt.value>(element(It, at));
+        rx[i].template load<nt.value>(element(xt, at));
+      }
+    });
+    float a[TT][V], u[TT][V], P[V], U[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float beta, g = 1.f;
-      decay_of<SCALE>(rA[i].get(v), a[i][v], beta);
-      if constexpr (GATE) g = sigmoid_v(rI[i].get(v));
-      u[i][v] = beta * g * rx[i].get(v);
-      U[v] = fmaf(a[i][v], U[v], u[i][v]);
-      P[v] *= a[i][v];
+      P[v] = 1.f;
+      U[v] = 0.f;
     }
-  }
-  scan_groups<TL, false>(P, U, lane, sp.c, j.P + wave * C, j.U + wave * C);
-  __syncthreads();
-  enter = join_tiles<TL, false>(j, wave, lane, exists, tiles > 1 ? tile : 0, tiles, enter,
-                                words + hs * slab_words(tiles, C));
-  float h[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = fmaf(P[v], j.H[wave * C + sp.c + v], U[v]);
-  const bool last = tile == tiles * runs - 1 && hf;
+    for (int i = 0; i < TT; ++i) {
+      rA[i].or_else(sp.tok + i < sp.rows, 0xff80u);  // tokens past the end leave the state alone:
+      rx[i].or_else(sp.tok + i < sp.rows, 0u);       // A_P = -inf, x = 0
 #pragma unroll
-  for (int i = 0; i < TT; ++i) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], u[i][v]);
-    if (sp.live && sp.tok + i < sp.rows) {
-      either(nt_row, [&](auto nt) { store_row<V, nt.value>(element(yt, sp.at(i, DH)), h); });
-      if (last && sp.tok + i == sp.rows - 1) store_row<V>(hf + state + sp.c, h);
+      for (int v = 0; v < V; ++v) {
+        float beta, g = 1.f;
+        decay_of<SCALE>(rA[i].get(v), a[i][v], beta);
+        if constexpr (GATE) g = sigmoid_v(rI[i].get(v));
+        u[i][v] = beta * g * rx[i].get(v);
+        U[v] = fmaf(a[i][v], U[v], u[i][v]);
+        P[v] *= a[i][v];
+      }
     }
-  }
+    scan_groups<TL, false>(P, U, lane, sp.c, j.P + wave * C, j.U + wave * C);
+    __syncthreads();
+    enter = join_tiles<TL, false>(j, wave, lane, exists, tiles > 1 ? tile : 0, tiles, enter,
+                                  words + hs * slab_words(tiles, C));
+    float h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = fmaf(P[v], j.H[wave * C + sp.c + v], U[v]);
+    const bool last = tile == tiles * runs - 1 && hf;
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], u[i][v]);
+      if (sp.live && sp.tok + i < sp.rows) {
+        either(nt_row, [&](auto nt) { store_row<V, nt.value>(element(yt, sp.at(i, DH)), h); });
+        if (last && sp.tok + i == sp.rows - 1) store_row<V>(hf + state + sp.c, h);
+      }
+    }
   }
 }
 
@@ -368,88 +373,88 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
   float enter = 0.f;  // in the first wave: d_final_state, then the c that leaves each tile
   if (wave == 0 && exists && dlast) enter = dlast[state + lane];
   for (int k = 0; k < runs; ++k) {
-  const int order = taken + k, tile = tiles * runs - 1 - order;
-  asm("" : "+s"(DH));  // a tile's offsets are not worth registers over the loop
-  const Spot<TL> sp(bh, start, tile, N, DH, width);
-  const T *xt = x + sp.base, *At = A + sp.base, *It = I + sp.base;
-  const float *dyt = dy + sp.base, *yt = y + sp.base - DH;  // yt: a row before, the states before each token
-  float *dxt = dx + sp.base, *dAt = dA + sp.base, *dIt = dI + sp.base;
-  const bool first = tile == 0 && sp.tok == 0;  // the sequence's first token: the state before it is h0
+    const int order = taken + k, tile = tiles * runs - 1 - order;
+    asm("" : "+s"(DH));  // a tile's offsets are not worth registers over the loop
+    const Spot<TL> sp(bh, start, tile, N, DH, width);
+    const T *xt = x + sp.base, *At = A + sp.base, *It = I + sp.base;
+    const float *dyt = dy + sp.base, *yt = y + sp.base - DH;  // yt: a row before, the states before each token
+    float *dxt = dx + sp.base, *dAt = dA + sp.base, *dIt = dI + sp.base;
+    const bool first = tile == 0 && sp.tok == 0;  // the sequence's first token: the state before it is h0
 
-  Raw<T, V> rA[TT], rx[TT], rI[TT];
-  Raw<float, V> rd[TT], rp[TT], r0;
-  either(nt_row, [&](auto nt) {
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      rA[i].template load<nt.value>(element(At, sp.at(i, DH)));
-      rd[i].template load<nt.value>(element(dyt, sp.at(i, DH)));
-    }
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      const unsigned at = sp.at(i, DH);
-      rx[i].template load<nt.value>(element(xt, at));
-      if constexpr (GATE) rI[i].template load<nt.value>(element(It, at));
-      // the row before; before the sequence's first row there is none, and its own is read without use
-      rp[i].template load<nt.value>(element(yt, tile == 0 && at < (unsigned)DH ? at + DH : at));
-    }
-  });
-  if (tile == 0 && h0) r0.load(h0 + state + sp.c);
-  float P[V], U[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    P[v] = 1.f;
-    U[v] = 0.f;
-  }
-#pragma unroll
-  for (int i = TT - 1; i >= 0; --i) {
-    rA[i].or_else(sp.tok + i < sp.rows, 0xff80u);  // tokens past the end: a = 1, dy = 0
-    rd[i].or_else(sp.tok + i < sp.rows, 0u);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float a, rest;
-      sigmoid_pair(rA[i].get(v), rest, a);
-      U[v] = a * (rd[i].get(v) + U[v]);
-      P[v] *= a;
-    }
-  }
-  scan_groups<TL, true>(P, U, lane, sp.c, j.P + wave * C, j.U + wave * C);
-  __syncthreads();
-  enter = join_tiles<TL, true>(j, wave, lane, exists, tiles > 1 ? order : 0, tiles, enter,
-                               words + hs * slab_words(tiles, C));
-  // the decays are computed again rather than held over the wait
-#pragma unroll
-  for (int i = 0; i < TT; ++i) rA[i].forget();
-  float carry[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) carry[v] = fmaf(P[v], j.H[wave * C + sp.c + v], U[v]);
-#pragma unroll
-  for (int i = TT - 1; i >= 0; --i) {
-    if (!sp.live || sp.tok + i >= sp.rows) continue;
-    float ox[V], oA[V], oI[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float a, rest, beta, db, g = 1.f;
-      decay_slope<SCALE>(rA[i].get(v), a, rest, beta, db);
-      const float lam = rd[i].get(v) + carry[v], xv = rx[i].get(v);
-      if constexpr (GATE) {
-        float ng;
-        sigmoid_pair(rI[i].get(v), g, ng);
-        oI[v] = lam * beta * xv * g * ng;
-      }
-      float prev = rp[i].get(v);
-      if (i == 0 && first) prev = h0 ? r0.get(v) : 0.f;
-      ox[v] = lam * beta * g;
-      oA[v] = lam * (SCALE == IN_PLAIN ? -(a * rest) * prev : fmaf(db * g, xv, -(a * rest) * prev));
-      carry[v] = a * lam;
-    }
-    const unsigned at = sp.at(i, DH);
+    Raw<T, V> rA[TT], rx[TT], rI[TT];
+    Raw<float, V> rd[TT], rp[TT], r0;
     either(nt_row, [&](auto nt) {
-      store_row<V, nt.value>(element(dxt, at), ox);
-      store_row<V, nt.value>(element(dAt, at), oA);
-      if constexpr (GATE) store_row<V, nt.value>(element(dIt, at), oI);
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        rA[i].template load<nt.value>(element(At, sp.at(i, DH)));
+        rd[i].template load<nt.value>(element(dyt, sp.at(i, DH)));
+      }
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        const unsigned at = sp.at(i, DH);
+        rx[i].template load<nt.value>(element(xt, at));
+        if constexpr (GATE) rI[i].template load<nt.value>(element(It, at));
+        // the row before; before the sequence's first row there is none, and its own is read without use
+        rp[i].template load<nt.value>(element(yt, tile == 0 && at < (unsigned)DH ? at + DH : at));
+      }
     });
-    if (i == 0 && first && dh0) store_row<V>(dh0 + state + sp.c, carry);
-  }
+    if (tile == 0 && h0) r0.load(h0 + state + sp.c);
+    float P[V], U[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      P[v] = 1.f;
+      U[v] = 0.f;
+    }
+#pragma unroll
+    for (int i = TT - 1; i >= 0; --i) {
+      rA[i].or_else(sp.tok + i < sp.rows, 0xff80u);  // tokens past the end: a = 1, dy = 0
+      rd[i].or_else(sp.tok + i < sp.rows, 0u);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float a, rest;
+        sigmoid_pair(rA[i].get(v), rest, a);
+        U[v] = a * (rd[i].get(v) + U[v]);
+        P[v] *= a;
+      }
+    }
+    scan_groups<TL, true>(P, U, lane, sp.c, j.P + wave * C, j.U + wave * C);
+    __syncthreads();
+    enter = join_tiles<TL, true>(j, wave, lane, exists, tiles > 1 ? order : 0, tiles, enter,
+                                 words + hs * slab_words(tiles, C));
+    // the decays are computed again rather than held over the wait
+#pragma unroll
+    for (int i = 0; i < TT; ++i) rA[i].forget();
+    float carry[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) carry[v] = fmaf(P[v], j.H[wave * C + sp.c + v], U[v]);
+#pragma unroll
+    for (int i = TT - 1; i >= 0; --i) {
+      if (!sp.live || sp.tok + i >= sp.rows) continue;
+      float ox[V], oA[V], oI[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float a, rest, beta, db, g = 1.f;
+        decay_slope<SCALE>(rA[i].get(v), a, rest, beta, db);
+        const float lam = rd[i].get(v) + carry[v], xv = rx[i].get(v);
+        if constexpr (GATE) {
+          float ng;
+          sigmoid_pair(rI[i].get(v), g, ng);
+          oI[v] = lam * beta * xv * g * ng;
+        }
+        float prev = rp[i].get(v);
+        if (i == 0 && first) prev = h0 ? r0.get(v) : 0.f;
+        ox[v] = lam * beta * g;
+        oA[v] = lam * (SCALE == IN_PLAIN ? -(a * rest) * prev : fmaf(db * g, xv, -(a * rest) * prev));
+        carry[v] = a * lam;
+      }
+      const unsigned at = sp.at(i, DH);
+      either(nt_row, [&](auto nt) {
+        store_row<V, nt.value>(element(dxt, at), ox);
+        store_row<V, nt.value>(element(dAt, at), oA);
+        if constexpr (GATE) store_row<V, nt.value>(element(dIt, at), oI);
+      });
+      if (i == 0 && first && dh0) store_row<V>(dh0 + state + sp.c, carry);
+    }
   }
 }
 
@@ -599,8 +604,8 @@ hipError_t launch_gated_scan(bool bf16, int scale, const void* x, const void* A,
     using TL = Tile<kind_v(k.value), kind_lpr(k.value), nw.value, fwd_tokens(sizeof(T) == 2)>;
     hipLaunchKernelGGL((k_gated_scan<T, sc.value, g.value, TL>), dim3((unsigned)(s.heads * s.tiles)),
                        dim3(TL::NW * WAVE), 0, stream, (const T*)x, (const T*)A, (const T*)I, h0, N,
-                       (int)DH, s.width, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs, passing(DH), y, hf, (unsigned*)ws,
-                       (word_t*)(ws + s.counters()));
+                       (int)DH, s.width, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs, passing(DH), y,
+                       hf, (unsigned*)ws, (word_t*)(ws + s.counters()));
     return hipGetLastError();
   });
 }
@@ -629,8 +634,8 @@ hipError_t launch_gated_scan_backward(bool bf16, int scale, const void* x, const
     using TL = Tile<kind_v(k.value), kind_lpr(k.value), nw.value, BWD_TOKENS>;
     hipLaunchKernelGGL((k_gated_scan_bwd<T, sc.value, g.value, TL>), dim3((unsigned)(s.heads * s.tiles)),
                        dim3(TL::NW * WAVE), 0, stream, (const T*)x, (const T*)A, (const T*)I, h0, y, dy,
-                       dlast, N, (int)DH, s.width, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs, passing(DH), dx, dA, dI, dh0,
-                       (unsigned*)ws, (word_t*)(ws + s.counters()));
+                       dlast, N, (int)DH, s.width, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs,
+                       passing(DH), dx, dA, dI, dh0, (unsigned*)ws, (word_t*)(ws + s.counters()));
     return hipGetLastError();
   });
 }

@@ -113,7 +113,8 @@ def scan_backward(x, A, I, h0, y, dy, dlast, scale):
     prev = _before(y, h0)
     dx = lam * beta * g
     dA = lam * (dbeta * g * x - a * rest * prev)
-    dI = None if I is None else lam * beta * x * g * (1 - g)
+    # 1 - g as sigmoid(-I): the difference has lost its digits from I = 36 on (e^-36 = 2^-52)
+    dI = None if I is None else lam * beta * x * g * sigmoid(-I)
     return dx, dA, dI, a[..., 0, :] * lam[..., 0, :]
 
 
@@ -134,7 +135,7 @@ def scan_backward_bound(x, A, I, h0, y, dy, dlast, scale):
     lam = U * (qs + (JOIN + 60 + 3 * size(A) + size(I)) * ms)
     prev = np.abs(_before(y, h0))
     dA = lam * (dbeta * g * np.abs(x) + a * rest * prev) + TINY
-    dI = None if I is None else lam * beta * np.abs(x) * g * (1 - g) + TINY
+    dI = None if I is None else lam * beta * np.abs(x) * g * sigmoid(-I) + TINY
     return lam * beta * g + TINY, dA, dI, (lam * a)[..., 0, :] + TINY
 
 

@@ -228,6 +228,57 @@ def test_scan_nonfinite_stays_in_its_channel(ssd, d, bad):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("d", [64, 5])
+def test_scan_wide_logits(ssd, d):
+    """Logits over all of the range that is not counted as infinite, and beyond."""
+    g = np.random.default_rng(12)
+    shape = (1, 2, 400, d)
+    logits = g.uniform(-85, 85, size=(2,) + shape)
+    t = [dev(g.standard_normal(shape)), dev(logits[0]), dev(logits[1])]
+    dy = dev(g.standard_normal(shape))
+    for scale in SCALES:
+        args = [f64(v) for v in t] + [None]
+        y = ssd.gated_scan(*t, scale=scale)
+        close(y, K.scan(*args, scale), K.scan_bound(*args, scale), "y")
+        got = ssd.gated_scan_backward(*t, y, dy, scale=scale)
+        args += [f64(y), f64(dy), None, scale]
+        for name, v, want, bound in zip(("dx", "dA", "dI"), got, K.scan_backward(*args), K.scan_backward_bound(*args)):
+            close(v, want, bound, name)
+    far = [t[0], t[1].sign() * 1e4, t[2].sign() * 1e4]
+    end = [t[0], t[1].sign() * float("inf"), t[2].sign() * float("inf")]
+    for scale in SCALES:
+        y = ssd.gated_scan(*far, scale=scale)
+        assert torch.equal(y, ssd.gated_scan(*end, scale=scale))
+        for a, b in zip(ssd.gated_scan_backward(*far, y, dy, scale=scale)[:3],
+                        ssd.gated_scan_backward(*end, y, dy, scale=scale)[:3]):
+            assert torch.equal(a, b) and bool(torch.isfinite(a).all())
+
+
+def test_padded_batch(ssd):
+    """Padding behind each sequence: logits of -inf keep the last state, and no gradient enters it."""
+    g = np.random.default_rng(13)
+    B, H, N, d, lengths = 3, 2, 700, 64, (700, 301, 1)
+    x, A, dl = g.standard_normal((B, H, N, d)), g.standard_normal((B, H, N, d)) - 3, g.standard_normal((B, H, d))
+    for b, n in enumerate(lengths):
+        A[b, :, n:] = -np.inf
+    t, dl = [dev(x, "bf16"), dev(A, "bf16"), None], dev(dl)
+    last = torch.empty((B, H, d), device="cuda")
+    y = ssd.gated_scan(*t, scale=2, final_state=last)
+    grads = ssd.gated_scan_backward(*t, y, torch.zeros_like(y), scale=2, d_final_state=dl)
+    for b, n in enumerate(lengths):
+        alone = [v[b:b + 1, :, :n].contiguous() for v in t[:2]] + [None]
+        one = torch.empty((1, H, d), device="cuda")
+        y1 = ssd.gated_scan(*alone, scale=2, final_state=one)
+        # the same sums, in other shares of the workgroups: a few roundings of the state
+        assert float((last[b] - one[0]).abs().max()) <= 100 * K.U * float(y1.abs().max() + 1)
+        assert torch.equal(last[b], y[b, :, -1])
+        g1 = ssd.gated_scan_backward(*alone, y1, torch.zeros_like(y1), scale=2, d_final_state=dl[b:b + 1])
+        for a, c in zip(grads[:2], g1[:2]):
+            assert bool((a[b, :, n:] == 0).all())
+            # lam after n steps: 9 roundings a step (the oracle's STEP) and the joins
+            assert float((a[b, :, :n] - c[0]).abs().max()) <= (9 * n + 200) * K.U * float(c.abs().max())
+
+
 def test_scan_empty(ssd):
     for B, H, N in ((0, 2, 5), (2, 0, 5), (2, 3, 0)):
         x = torch.zeros((B, H, N, 8), device="cuda")

@@ -519,13 +519,14 @@ constexpr int fwd_tokens(bool bf16) { return bf16 ? 8 : 4; }
 constexpr int BWD_TOKENS = 4;
 
 // How a call is cut.  A workgroup of 16 waves has the larger tile, so fewer
-// steps to publish and wait for, but a CU holds only one; two of 8 waves take
-// turns at loading and storing.  16 waves where there are at most 512 of their
-// tiles (4 heads x 16 of 2048 tokens, bf16: 18.8 us against 21.0; backwards 45.7
-// against 51.0), 8 beyond (8192 tokens: 65.8 against 72.3).  With 512 heads and
-// slabs or more the chip is full without cutting sequences: a workgroup runs
-// its head's tiles one after the other and nothing is published (32 x 16 heads
-// of 2048 tokens: 121 us against 125).
+// steps to publish and wait for, but a CU holds only one: it pays where its tiles
+// fill the 256 CUs in whole rounds, up to three and a half (4 x 16 heads of 2048
+// tokens, bf16, one round: 18.1 us against 20.6 of 8 waves; backwards, two: 45.8
+// against 48.8).  Else two workgroups of 8 waves take turns at loading and
+// storing (4 x 16 of 2304 tokens, 1.25 rounds: 24.6 us against 27.0; of 8192, four:
+// 64.9 against 66.0).  With 512 heads and slabs or more the chip is then full
+// without cutting sequences: a workgroup runs its head's tiles one after the
+// other and nothing is published (32 x 16 heads of 2000 tokens: 126 us against 130).
 struct Split {
   int64_t slabs, heads, tiles;  // tiles: those that workgroups of one head share out
   int waves, runs, C, width;    // runs: tiles that a workgroup takes one after the other (then tiles = 1);
@@ -543,7 +544,9 @@ static Split split_of(int64_t BH, int64_t N, int64_t DH, int tokens) {
     const int64_t per = (int64_t)waves * (WAVE / lpr) * tokens;
     return (N + per - 1) / per;
   };
-  if (heads * tiles(16) <= 512) return {slabs, heads, tiles(16), 16, 1, C, width};
+  const int64_t wide = heads * tiles(16), rounds = (wide + 255) / 256;
+  if (rounds <= 1 || (wide < 4 * 256 && 4 * wide > 3 * 256 * rounds))
+    return {slabs, heads, tiles(16), 16, 1, C, width};
   if (heads >= 512) return {slabs, heads, 1, 8, (int)tiles(8), C, width};
   return {slabs, heads, tiles(8), 8, 1, C, width};
 }

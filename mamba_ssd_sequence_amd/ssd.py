@@ -480,13 +480,13 @@ def prep_amask_backward(A_proj, dt_proj, da, ddt=None):
 # message is made only when it fails), and the stream is taken as a number.
 
 
-def _refuse(t, name, dtype, shape, device):
+def _refuse(t, name, dtype, shape, index):
     """Why a tensor was refused."""
-    _require(t, name, dtype, device)
+    _require(t, name, dtype, _torch().device("cuda", index))
     raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _at(t, name, dtype, shape, index, device):
+def _at(t, name, dtype, shape, index):
     """The address of a call's tensor after its checks (None for None)."""
     if t is None:
         return None
@@ -495,30 +495,45 @@ def _at(t, name, dtype, shape, index, device):
             return t.data_ptr()
     except AttributeError:
         pass
-    _refuse(t, name, dtype, shape, device)
+    _refuse(t, name, dtype, shape, index)
 
 
 def _first(t, name):
-    """The checks of the tensor that sets a call's sizes; returns its element type and device."""
+    """The checks of a tensor that sets a call's sizes; returns its element type and device index."""
+    try:
+        index, kind = t.get_device(), _kinds().get(t.dtype)
+        if index >= 0 and kind is not None and t.is_contiguous():
+            return kind, index
+    except AttributeError:
+        pass
     _require(t, name)
-    return _qkv_dtype(t), t.device
+    raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
 
-def _raw_stream(index):
+@functools.lru_cache(maxsize=1)
+def _kinds():
     torch = _torch()
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+    return {torch.bfloat16: SSD_BF16, torch.float32: SSD_F32}
+
+
+@functools.lru_cache(maxsize=1)
+def _current():
+    """Functions for the current device's index and a device's current stream as a number."""
+    torch = _torch()
+    device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return device, stream or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _call(fn, index, *args):
     """fn(*args, stream) on the arrays' device and its current stream (the
     library launches on the current device)."""
-    torch = _torch()
-    if index == torch.cuda.current_device():
-        status = fn(*args, _raw_stream(index))
+    device, stream = _current()
+    if index == device():
+        status = fn(*args, stream(index))
     else:
-        with torch.cuda.device(index):
-            status = fn(*args, _raw_stream(index))
+        with _torch().cuda.device(index):
+            status = fn(*args, stream(index))
     if status != SSD_OK:
         _check(status)
 
@@ -528,14 +543,14 @@ def _scratch_size(name, *sizes):
     return int(getattr(lib(), name)(*sizes))
 
 
-def _scratch(workspace, need, device):
-    """A call's workspace: (address, bytes, tensor); one is allocated when None is given."""
+def _scratch(workspace, need, like):
+    """A call's workspace: (address, bytes, tensor); one is allocated on like's device when None is given."""
     if workspace is None:
         if not need:
             return None, 0, None
-        workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+        workspace = _torch().empty(need, dtype=_torch().uint8, device=like.device)
         return workspace.data_ptr(), need, workspace
-    _require(workspace, "workspace", None, device)
+    _require(workspace, "workspace", None, like.device)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -545,17 +560,16 @@ def gated_scan(x, A_proj, I_proj=None, *, scale: int, initial_state=None, final_
     (or 1) and beta by scale (SSD_INPUT_PLAIN, _CONVEX, _UNIT).  x, A_proj, I_proj [B,H,N,d_h] bf16 or
     fp32, states [B,H,d_h] fp32 (final_state is written when given); returns y [B,H,N,d_h] fp32."""
     torch = _torch()
-    kind, dev = _first(x, "x")
-    i, f32, xt, shape = dev.index, torch.float32, x.dtype, x.shape
+    kind, i = _first(x, "x")
+    f32, xt, shape = torch.float32, x.dtype, x.shape
     B, H, N, d_h = shape
     state = (B, H, d_h)
     if y is None:
-        y = torch.empty(shape, dtype=f32, device=dev)
-    ws, nbytes, keep = _scratch(workspace, _scratch_size("ssd_gated_scan_workspace_size", B, H, N, d_h), dev)
-    _call(lib().ssd_gated_scan, i, x.data_ptr(), _at(A_proj, "A_proj", xt, shape, i, dev),
-          _at(I_proj, "I_proj", xt, shape, i, dev), _at(initial_state, "initial_state", f32, state, i, dev),
-          B, H, N, d_h, scale, kind, _at(y, "y", f32, shape, i, dev),
-          _at(final_state, "final_state", f32, state, i, dev), ws, nbytes)
+        y = torch.empty_like(x, dtype=f32)
+    ws, nbytes, keep = _scratch(workspace, _scratch_size("ssd_gated_scan_workspace_size", B, H, N, d_h), x)
+    _call(lib().ssd_gated_scan, i, x.data_ptr(), _at(A_proj, "A_proj", xt, shape, i),
+          _at(I_proj, "I_proj", xt, shape, i), _at(initial_state, "initial_state", f32, state, i), B, H, N, d_h,
+          scale, kind, _at(y, "y", f32, shape, i), _at(final_state, "final_state", f32, state, i), ws, nbytes)
     return y
 
 
@@ -563,14 +577,14 @@ def gated_scan_step(x, A_proj, I_proj, state, *, scale: int, new_state=None):
     """ssd_gated_scan_step: one token of S sequences, x, A_proj, I_proj (or None) [S,H,d_h], state
     [S,H,d_h] fp32.  The state is updated in place unless new_state is given; returns the new state,
     which is the step's output."""
-    kind, dev = _first(x, "x")
-    i, f32, xt, shape = dev.index, _torch().float32, x.dtype, x.shape
+    kind, i = _first(x, "x")
+    f32, xt, shape = _torch().float32, x.dtype, x.shape
     S, H, d_h = shape
     if new_state is None:
         new_state = state
-    _call(lib().ssd_gated_scan_step, i, x.data_ptr(), _at(A_proj, "A_proj", xt, shape, i, dev),
-          _at(I_proj, "I_proj", xt, shape, i, dev), _at(state, "state", f32, shape, i, dev), S, H, d_h, scale, kind,
-          _at(new_state, "new_state", f32, shape, i, dev))
+    _call(lib().ssd_gated_scan_step, i, x.data_ptr(), _at(A_proj, "A_proj", xt, shape, i),
+          _at(I_proj, "I_proj", xt, shape, i), _at(state, "state", f32, shape, i), S, H, d_h, scale, kind,
+          _at(new_state, "new_state", f32, shape, i))
     return new_state
 
 
@@ -580,20 +594,20 @@ def gated_scan_backward(x, A_proj, I_proj, y, dy, *, scale: int, initial_state=N
     (None without initial_state), all fp32.  y: gated_scan's output; dy, d_final_state (or None): the
     gradients with respect to y and the final state."""
     torch = _torch()
-    kind, dev = _first(x, "x")
-    i, f32, xt, shape = dev.index, torch.float32, x.dtype, x.shape
+    kind, i = _first(x, "x")
+    f32, xt, shape = torch.float32, x.dtype, x.shape
     B, H, N, d_h = shape
     state = (B, H, d_h)
-    py, ph0 = _at(y, "y", f32, shape, i, dev), _at(initial_state, "initial_state", f32, state, i, dev)
+    py, ph0 = _at(y, "y", f32, shape, i), _at(initial_state, "initial_state", f32, state, i)
     if y is None:
         raise TypeError("y must be a torch.Tensor")
     dx, dA = torch.empty_like(y), torch.empty_like(y)
     dI = torch.empty_like(y) if I_proj is not None else None
     dh0 = torch.empty_like(initial_state) if initial_state is not None else None
-    ws, nbytes, keep = _scratch(workspace, _scratch_size("ssd_gated_scan_backward_workspace_size", B, H, N, d_h), dev)
-    _call(lib().ssd_gated_scan_backward, i, x.data_ptr(), _at(A_proj, "A_proj", xt, shape, i, dev),
-          _at(I_proj, "I_proj", xt, shape, i, dev), ph0, py, _at(dy, "dy", f32, shape, i, dev),
-          _at(d_final_state, "d_final_state", f32, state, i, dev), B, H, N, d_h, scale, kind, dx.data_ptr(),
+    ws, nbytes, keep = _scratch(workspace, _scratch_size("ssd_gated_scan_backward_workspace_size", B, H, N, d_h), x)
+    _call(lib().ssd_gated_scan_backward, i, x.data_ptr(), _at(A_proj, "A_proj", xt, shape, i),
+          _at(I_proj, "I_proj", xt, shape, i), ph0, py, _at(dy, "dy", f32, shape, i),
+          _at(d_final_state, "d_final_state", f32, state, i), B, H, N, d_h, scale, kind, dx.data_ptr(),
           dA.data_ptr(), dI.data_ptr() if dI is not None else None, dh0.data_ptr() if dh0 is not None else None,
           ws, nbytes)
     return dx, dA, dI, dh0
@@ -605,9 +619,10 @@ def norm_in(residual, branch, branch_scale, weight, eps: float, *, dtype=None, r
     is u's type); branch_scale [E] fp32 or None (1).  Returns (r' fp32, u of branch's type)."""
     torch = _torch()
     f32 = torch.float32
-    _require(residual, "residual", f32)
-    dev, shape = residual.device, residual.shape
-    i, E = dev.index, shape[-1]
+    i = _first(residual, "residual")[1]
+    shape = residual.shape
+    E = shape[-1]
+    at = _at(residual, "residual", f32, shape, i)
     if branch is not None:
         dtype = branch.dtype
         if residual_out is None:
@@ -616,9 +631,9 @@ def norm_in(residual, branch, branch_scale, weight, eps: float, *, dtype=None, r
         out = torch.empty_like(residual, dtype=dtype)
     kind, dtype = _qkv_dtype(out), (out.dtype if dtype is None else dtype)
     rows = residual.numel() // E if E else 0
-    _call(lib().ssd_norm_in, i, residual.data_ptr(), _at(branch, "branch", dtype, shape, i, dev),
-          _at(branch_scale, "branch_scale", f32, (E,), i, dev), _at(weight, "weight", f32, (E,), i, dev), rows, E,
-          eps, kind, _at(residual_out, "residual_out", f32, shape, i, dev), _at(out, "out", dtype, shape, i, dev))
+    _call(lib().ssd_norm_in, i, at, _at(branch, "branch", dtype, shape, i),
+          _at(branch_scale, "branch_scale", f32, (E,), i), _at(weight, "weight", f32, (E,), i), rows, E,
+          eps, kind, _at(residual_out, "residual_out", f32, shape, i), _at(out, "out", dtype, shape, i))
     return (residual if branch is None else residual_out), out
 
 
@@ -629,25 +644,24 @@ def norm_in_backward(d_out, d_residual_out, residual_out, branch, branch_scale, 
     is then not read.  d_residual_out: fp32, or None (zero); residual_out: the r' of norm_in."""
     torch = _torch()
     f32 = torch.float32
-    kind, dev = _first(d_out, "d_out")
+    kind, i = _first(d_out, "d_out")
     shape = d_out.shape
-    i, E = dev.index, shape[-1]
+    E = shape[-1]
     if branch_scale is not None and branch is None:
         raise ValueError("branch_scale without branch")
     if branch_scale is None:
         branch = None
     rows = d_out.numel() // E if E else 0
-    pr, pw = _at(residual_out, "residual_out", f32, shape, i, dev), _at(weight, "weight", f32, (E,), i, dev)
+    pr, pw = _at(residual_out, "residual_out", f32, shape, i), _at(weight, "weight", f32, (E,), i)
     if residual_out is None or weight is None:
         raise TypeError("residual_out and weight must be torch.Tensors")
     d_residual, d_weight = torch.empty_like(residual_out), torch.empty_like(weight)
     d_branch = torch.empty_like(residual_out) if branch is not None else None
     d_scale = torch.empty_like(weight) if branch is not None else None
-    ws, nbytes, keep = _scratch(workspace, _scratch_size("ssd_norm_in_backward_workspace_size", rows, E), dev)
-    _call(lib().ssd_norm_in_backward, i, d_out.data_ptr(),
-          _at(d_residual_out, "d_residual_out", f32, shape, i, dev), pr,
-          _at(branch, "branch", d_out.dtype, shape, i, dev), _at(branch_scale, "branch_scale", f32, (E,), i, dev),
-          pw, rows, E, eps, kind, d_residual.data_ptr(),
+    ws, nbytes, keep = _scratch(workspace, _scratch_size("ssd_norm_in_backward_workspace_size", rows, E), d_out)
+    _call(lib().ssd_norm_in_backward, i, d_out.data_ptr(), _at(d_residual_out, "d_residual_out", f32, shape, i), pr,
+          _at(branch, "branch", d_out.dtype, shape, i), _at(branch_scale, "branch_scale", f32, (E,), i), pw, rows, E,
+          eps, kind, d_residual.data_ptr(),
           d_branch.data_ptr() if branch is not None else None, d_weight.data_ptr(),
           d_scale.data_ptr() if branch is not None else None, ws, nbytes)
     return d_residual, (d_residual if d_branch is None else d_branch), d_weight, d_scale
@@ -657,16 +671,16 @@ def norm_out(y, z, weight, eps: float, *, groups: int = 1, gate_first: bool = Tr
     """ssd_norm_out: the mixer's y [B,H,N,d_h] fp32, gated by silu(z) and normalised over `groups` groups of a
     token's channels, in token order: z and the result [B,N,H d_h] bf16 or fp32, weight [H d_h] fp32."""
     torch = _torch()
-    kind, dev = _first(z, "z")
-    i, zt = dev.index, z.dtype
-    _require(y, "y", torch.float32, dev)
+    kind, i = _first(z, "z")
+    zt = z.dtype
+    py = _at(y, "y", torch.float32, y.shape, i)
     B, H, N, d_h = y.shape
     shape = (B, N, H * d_h)
     if out is None:
         out = torch.empty_like(z)
-    _call(lib().ssd_norm_out, i, y.data_ptr(), _at(z, "z", zt, shape, i, dev),
-          _at(weight, "weight", torch.float32, (H * d_h,), i, dev), B, H, N, d_h, groups, 1 if gate_first else 0, eps,
-          kind, _at(out, "out", zt, shape, i, dev))
+    _call(lib().ssd_norm_out, i, py, _at(z, "z", zt, shape, i),
+          _at(weight, "weight", torch.float32, (H * d_h,), i), B, H, N, d_h, groups, 1 if gate_first else 0, eps,
+          kind, _at(out, "out", zt, shape, i))
     return out
 
 
@@ -675,18 +689,18 @@ def norm_out_backward(d_out, y, z, weight, eps: float, *, groups: int = 1, gate_
     """ssd_norm_out_backward: returns dy [B,H,N,d_h], dz [B,N,H d_h], d_weight [H d_h], all fp32."""
     torch = _torch()
     f32 = torch.float32
-    kind, dev = _first(z, "z")
-    i, zt = dev.index, z.dtype
-    _require(y, "y", f32, dev)
+    kind, i = _first(z, "z")
+    zt = z.dtype
+    py = _at(y, "y", f32, y.shape, i)
     B, H, N, d_h = y.shape
     shape = (B, N, H * d_h)
-    pw = _at(weight, "weight", f32, (H * d_h,), i, dev)
+    pw = _at(weight, "weight", f32, (H * d_h,), i)
     if weight is None:
         raise TypeError("weight must be a torch.Tensor")
     dy, dz, d_weight = torch.empty_like(y), torch.empty_like(z, dtype=f32), torch.empty_like(weight)
     ws, nbytes, keep = _scratch(workspace,
-                                _scratch_size("ssd_norm_out_backward_workspace_size", B, H, N, d_h, groups), dev)
-    _call(lib().ssd_norm_out_backward, i, _at(d_out, "d_out", zt, shape, i, dev), y.data_ptr(),
-          _at(z, "z", zt, shape, i, dev), pw, B, H, N, d_h, groups,
-          1 if gate_first else 0, eps, kind, dy.data_ptr(), dz.data_ptr(), d_weight.data_ptr(), ws, nbytes)
+                                _scratch_size("ssd_norm_out_backward_workspace_size", B, H, N, d_h, groups), z)
+    _call(lib().ssd_norm_out_backward, i, _at(d_out, "d_out", zt, shape, i), py, _at(z, "z", zt, shape, i), pw, B, H,
+          N, d_h, groups, 1 if gate_first else 0, eps, kind, dy.data_ptr(), dz.data_ptr(), d_weight.data_ptr(), ws,
+          nbytes)
     return dy, dz, d_weight

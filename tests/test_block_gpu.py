@@ -606,6 +606,51 @@ def every_call(ssd, seed):
     ]
 
 
+def test_refused_on_the_gpu(ssd):
+    """What the binding refuses of GPU tensors: types, shapes, strides, one operand on the host."""
+    x = torch.randn((1, 2, 8, 4), device="cuda")
+    h = torch.zeros((1, 2, 4), device="cuda")
+    w, rows = torch.ones(4, device="cuda"), torch.randn((6, 4), device="cuda")
+    wide = torch.randn((1, 2, 8, 8), device="cuda")[..., ::2]
+    bad = [
+        lambda: ssd.gated_scan(x, x.bfloat16(), scale=0),
+        lambda: ssd.gated_scan(x.half(), x.half(), scale=0),
+        lambda: ssd.gated_scan(x, x[:, :, :4].contiguous(), scale=0),
+        lambda: ssd.gated_scan(wide, x, scale=0),
+        lambda: ssd.gated_scan(x, wide, scale=0),
+        lambda: ssd.gated_scan(x, x.cpu(), scale=0),
+        lambda: ssd.gated_scan(x, x, scale=0, initial_state=x),
+        lambda: ssd.gated_scan(x, x, scale=0, y=x.bfloat16()),
+        lambda: ssd.gated_scan_step(x[:, :, 0].contiguous(), x[:, :, 1].contiguous(), None, h.cpu(), scale=0),
+        lambda: ssd.gated_scan_backward(x, x, None, x.bfloat16(), x, scale=0),
+        lambda: ssd.norm_in(rows.bfloat16(), rows, None, w, EPS),
+        lambda: ssd.norm_in(rows, rows[:5], None, w, EPS),
+        lambda: ssd.norm_in(rows, rows, w[:3], w, EPS),
+        lambda: ssd.norm_in(rows, rows, None, w, EPS, out=rows.bfloat16()),
+        lambda: ssd.norm_in_backward(rows, None, rows, None, w, w, EPS),
+        lambda: ssd.norm_in_backward(rows, None, rows.cpu(), None, None, w, EPS),
+        lambda: ssd.norm_out(x, rows, w, EPS),
+        lambda: ssd.norm_out(x, torch.randn((1, 8, 8), device="cuda"), w, EPS),
+        lambda: ssd.norm_out_backward(rows, x, torch.randn((1, 8, 8), device="cuda"), torch.ones(8, device="cuda"), EPS),
+    ]
+    for k, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            print("not refused:", k)
+    for f in (lambda: ssd.gated_scan(x, None, scale=0), lambda: ssd.gated_scan(x, x, scale=3),
+              lambda: ssd.gated_scan(x, x, scale=0, y=x), lambda: ssd.norm_in(rows, rows, None, w, -1.0),
+              lambda: ssd.norm_in(rows, rows, None, w, EPS, residual_out=rows),
+              lambda: ssd.gated_scan(x, x, scale=0, initial_state=h, final_state=h),
+              lambda: ssd.norm_out(x, torch.randn((1, 8, 8), device="cuda"), torch.ones(8, device="cuda"), EPS, groups=3)):
+        with pytest.raises(ssd.SSDError):
+            f()
+    for f in (lambda: ssd.gated_scan_backward(x, x, None, None, x, scale=0),
+              lambda: ssd.norm_in_backward(rows, None, None, None, None, w, EPS),
+              lambda: ssd.norm_in(None, rows, None, w, EPS)):
+        with pytest.raises(TypeError):
+            f()
+
+
 def test_same_bits_every_time(ssd):
     for name, f in every_call(ssd, 21):
         first = f()

@@ -695,8 +695,11 @@ static bool is_long(int64_t heads, int64_t width) {
 
 // calls f(R) with the row shape for `heads` heads of `width` channels: 8 channels
 // a thread (4 in rows of up to 256), so that a row with its weights and their
-// gradients leaves room for 16 waves a CU and more.
-template <typename F>
+// gradients leaves room for 16 waves a CU and more.  DEEP: 16 channels a thread, a
+// wave to a row of 1024, for norm out forwards, which holds least and whose rows
+// come from many places (2 x 16 heads of 8192 tokens: 23.0 us against 26.9, of 4096
+// 12.1 against 12.8; 1 x 16 of 65536 96 against 92; norm in 8192 rows 16.8 against 16.0).
+template <bool DEEP, typename F>
 static auto by_row(int64_t heads, int64_t width, F&& f) {
   const int64_t n = row_pieces(heads, width);
   if (width < 4) {
@@ -707,6 +710,12 @@ static auto by_row(int64_t heads, int64_t width, F&& f) {
   if (n <= 32) return f(Row<4, 32, 1>{});
   if (n <= 64) return f(Row<4, 64, 1>{});
   if (n <= 128) return f(Row<4, 64, 2>{});
+  if constexpr (DEEP) {
+    if (n <= 256) return f(Row<4, 64, 4>{});
+    if (n <= 512) return f(Row<4, 128, 4>{});
+    if (n <= 1024) return f(Row<4, 256, 4>{});
+    return f(Row<4, 512, 4>{});
+  }
   if (n <= 256) return f(Row<4, 128, 2>{});
   if (n <= 512) return f(Row<4, 256, 2>{});
   if (n <= 1024) return f(Row<4, 512, 2>{});
@@ -744,8 +753,8 @@ static Geo geo_of(R, int64_t tokens, int64_t groups, int64_t heads, int64_t widt
 
 static Geo geo_by(int64_t tokens, int64_t groups, int64_t heads, int64_t width, bool backward,
                   int64_t bytes) {
-  return by_row(heads, width,
-                [&](auto row) { return geo_of(row, tokens, groups, heads, width, backward, bytes); });
+  return by_row<false>(heads, width,
+                       [&](auto row) { return geo_of(row, tokens, groups, heads, width, backward, bytes); });
 }
 
 // Long rows: the rows' grid, and the backward's blocks of 256 pieces x parts of
@@ -781,9 +790,9 @@ static hipError_t launch_sum_parts(const float* part, int n, int64_t E, float* o
 }
 
 // calls f(T, row)
-template <typename F>
+template <bool DEEP = false, typename F>
 static hipError_t by_call(bool bf16, int64_t heads, int64_t width, F&& f) {
-  return by_row(heads, width, [&](auto row) { return bf16 ? f(uint16_t{}, row) : f(float{}, row); });
+  return by_row<DEEP>(heads, width, [&](auto row) { return bf16 ? f(uint16_t{}, row) : f(float{}, row); });
 }
 
 hipError_t launch_norm_in(bool bf16, const float* r, const void* p, const float* s, const float* w,
@@ -862,7 +871,7 @@ hipError_t launch_norm_out(bool bf16, bool gate_first, const float* y, const voi
       };
       return gate_first ? go(std::true_type{}) : go(std::false_type{});
     });
-  return by_call(bf16, H / groups, DH, [&](auto t, auto row) {
+  return by_call<true>(bf16, H / groups, DH, [&](auto t, auto row) {
     using T = decltype(t);
     using R = decltype(row);
     const Geo q = geo_of(row, B * N, groups, H / groups, DH, false, B * N * H * DH * (bf16 ? 8 : 12));

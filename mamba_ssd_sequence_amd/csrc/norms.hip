@@ -9,7 +9,7 @@
 // outputs, and norm out reads y where the mixer left it.  bf16, E 1024: norm in
 // 65536 rows 805 MB in 140 us (5.7 TB/s), backwards 8192 rows 168 MB in 33.5 us with
 // the sum of the weight gradients (4 us); norm out 2 x 16 heads of 4096 tokens 67 MB
-// in 12.9 us, backwards 4 x 16 of 2048 134 MB in 26.9 us.
+// in 12.1 us, backwards 4 x 16 of 2048 134 MB in 26.9 us.
 //
 // A row belongs to TPR threads, each with NV pieces of V channels; a workgroup
 // holds NT / TPR rows at a time and walks over the tokens, so that the weights

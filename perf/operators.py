@@ -235,7 +235,7 @@ def _norm_out_plain(y, z, w, groups, gate_first, dt):
     t = y * gate if gate_first else y
     n = t * (torch.mean(t * t, -1, keepdim=True) + EPS).rsqrt()
     o = n * w.view(groups, -1) if gate_first else n * w.view(groups, -1) * gate
-    return o.reshape(B, N, H * d).to(dt)
+    return o.view(B, N, H * d).to(dt)
 
 
 def _norm_out_back_plain(do, y, z, w, groups, gate_first):
@@ -252,8 +252,7 @@ def _norm_out_back_plain(do, y, z, w, groups, gate_first):
         dy, dz, dw = dt * gate, dt * y * slope, (do * t * k).sum((0, 1))
     else:
         dy, dz, dw = dt, do * w * y * k * slope, (do * y * k * gate).sum((0, 1))
-    return {"dy": dy.reshape(B, N, H, d).transpose(1, 2).contiguous(), "dz": dz.reshape(B, N, H * d),
-            "dw": dw.reshape(-1)}
+    return {"dy": dy.view(B, N, H, d).transpose(1, 2).contiguous(), "dz": dz.view(B, N, H * d), "dw": dw.view(-1)}
 
 
 def run(state):

@@ -489,10 +489,12 @@ ssd_status ssd_gated_scan_backward(const void* x, const void* A_proj, const void
  * weight per channel, a SiLU gate and a residual scale per channel.
  * Outgoing gradients are f32, as ssd_backward's; an incoming gradient has the
  * type of its array.  eps >= 0; with eps = 0 a row of zeros gives NaN, as the
- * quotient does.  Sums of squares and gradient sums are fp32 (a row whose squares
- * pass its range, values around 1e19, comes out as zeros); the weight gradients
- * are summed over rows in a fixed order (deterministic).  A workspace serves one
- * call at a time.
+ * quotient does.  Sums of squares and gradient sums are fp32: a row whose squares
+ * pass its range, values around 1e19, comes out as zeros; with eps = 0 a row whose
+ * squares fall below its normal numbers, values around 1e-19, loses digits, and
+ * one whose squares vanish, values under 1e-23, comes out infinite.  Between these
+ * outputs and gradients keep fp32's digits.  The weight gradients are summed over
+ * rows in a fixed order (deterministic).  A workspace serves one call at a time.
  *
  * ssd_norm_in -- what the previous block's output projection made is scaled
  * and added to the residual stream, whose RMS norm is the next block's input:
@@ -512,9 +514,9 @@ ssd_status ssd_norm_in(const float* residual, const void* branch, const float* b
                        float* residual_out, void* out, hipStream_t stream);
 
 /*
- * ssd_norm_in_backward -- with c = du w, k = 1 / sqrt(mean r'^2 + eps):
- *     dr = dr' + k c - k^3 mean(c r') r',   dp = s dr,
- *     dw = sum over rows of du r' k,        ds = sum over rows of dr p
+ * ssd_norm_in_backward -- with c = du w, k = 1 / sqrt(mean r'^2 + eps), n = r' k:
+ *     dr = dr' + k (c - n mean(c n)),   dp = s dr,
+ *     dw = sum over rows of du n,       ds = sum over rows of dr p
  *
  *   d_out          [rows,E] dtype  du
  *   d_residual_out [rows,E] f32    dr', or NULL (zero)
@@ -555,11 +557,11 @@ ssd_status ssd_norm_out(const float* y, const void* z, const float* weight, int6
                         int dtype, void* out, hipStream_t stream);
 
 /*
- * ssd_norm_out_backward -- with k = 1 / sqrt(mean_group t^2 + eps), t = y silu(z):
- *   gate_first 1:  dt = k do w - k^3 mean_group(do w t) t,
- *                  dy = dt silu(z),  dz = dt y silu'(z),  dw = sum do t k
- *   gate_first 0:  (t = y)  c = do w silu(z),  dy = k c - k^3 mean_group(c y) y,
- *                  dz = do w y k silu'(z),  dw = sum do y k silu(z)
+ * ssd_norm_out_backward -- with k = 1 / sqrt(mean_group t^2 + eps), n = t k:
+ *   gate_first 1:  t = y silu(z), c = do w,  dt = k (c - n mean_group(c n)),
+ *                  dy = dt silu(z),  dz = dt y silu'(z),  dw = sum do n
+ *   gate_first 0:  t = y, c = do w silu(z),  dy = k (c - n mean_group(c n)),
+ *                  dz = do w n silu'(z),  dw = sum do n silu(z)
  *
  *   d_out     [B,N,H d_h] dtype  do
  *   dy        [B,H,N,d_h] f32    out (as ssd_backward and ssd_gated_scan_backward take it)

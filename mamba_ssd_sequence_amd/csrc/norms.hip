@@ -4,6 +4,10 @@
 //     norm out:  t = y silu(z), o = w t k   or   o = w silu(z) y k,
 //                k over the groups of a token's channels; y in head order
 //                [B,H,N,d_h], z and o in token order [B,N,H d_h]
+// Backwards with t^ = t k, the row over its own size:
+//     dt = k (c - t^ mean(c t^)),  mean(c t^) = k mean(c t),
+// so that no power of k is formed: k^3 leaves fp32's range at rows of 1e13 (and,
+// with eps = 0, of 1e-13) while the gradients and the squares are well inside it.
 // All four are bound by memory: every array is read once and written once, a
 // row (a token's group of channels) lives in registers between its sums and its
 // outputs, and norm out reads y where the mixer left it.  bf16, E 1024: norm in
@@ -257,16 +261,16 @@ __global__ __launch_bounds__(R::NT) void k_norm_in_bwd(
       }
     }
     row_sums<R>(sq, cr, turn);
-    const float inv = inv_rms(sq, inv_n, eps), m = inv * inv * inv * (cr * inv_n);
+    const float inv = inv_rms(sq, inv_n, eps), m = inv * (cr * inv_n);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       float g[V], h[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float y = rr[k].get(v), d = rd[k].get(v);
-        g[v] = fmaf(-m, y, inv * (d * rw[k].get(v)));
+        const float hat = rr[k].get(v) * inv, d = rd[k].get(v);
+        g[v] = inv * fmaf(-m, hat, d * rw[k].get(v));
         if constexpr (ADDED) g[v] += ro[k].get(v);
-        dw[k][v] = live ? fmaf(d, y * inv, dw[k][v]) : dw[k][v];
+        dw[k][v] = live ? fmaf(d, hat, dw[k][v]) : dw[k][v];
         if constexpr (SCALED) {
           h[v] = rs[k].get(v) * g[v];
           ds[k][v] = live ? fmaf(g[v], rp[k].get(v), ds[k][v]) : ds[k][v];
@@ -364,16 +368,16 @@ __global__ __launch_bounds__(R::NT) void k_norm_out(const float* __restrict__ y,
   }
 }
 
-// One channel's gradients: k = inv, m = k^3 mean(c x).
+// One channel's gradients: k = inv, m = k mean(c x).
 template <bool FIRST>
 __device__ __forceinline__ void norm_out_slopes(float z, float y, float d, float w, float inv, float m,
                                                 float& dy, float& dz, float& dw) {
   const float sig = sigmoid_v(z), gate = z * sig, slope = sig * fmaf(z, 1.f - sig, 1.f);
-  const float c = d * w, x = FIRST ? y * gate : y;
-  const float dx = fmaf(-m, x, inv * (FIRST ? c : c * gate));
+  const float c = d * w, hat = (FIRST ? y * gate : y) * inv;
+  const float dx = inv * fmaf(-m, hat, FIRST ? c : c * gate);
   dy = FIRST ? dx * gate : dx;
-  dz = FIRST ? dx * y * slope : c * (y * inv) * slope;
-  dw = fmaf(FIRST ? d : d * gate, x * inv, dw);
+  dz = FIRST ? dx * y * slope : c * hat * slope;
+  dw = fmaf(FIRST ? d : d * gate, hat, dw);
 }
 
 template <typename T, typename R, bool FIRST>
@@ -423,7 +427,7 @@ __global__ __launch_bounds__(R::NT) void k_norm_out_bwd(
       }
     }
     row_sums<R>(sq, ct, turn);
-    const float inv = inv_rms(sq, inv_n, eps), m = inv * inv * inv * (ct * inv_n);
+    const float inv = inv_rms(sq, inv_n, eps), m = inv * (ct * inv_n);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       float gy[V], gz[V];
@@ -497,7 +501,7 @@ __global__ __launch_bounds__(LT) void k_long_in(const float* __restrict__ r, con
   }
 }
 
-// k and k^3 mean(c r) of every row
+// k and k mean(c r) of every row
 template <typename T, int V>
 __global__ __launch_bounds__(LT) void k_long_in_means(const T* __restrict__ du, const float* __restrict__ r,
                                                       const float* __restrict__ w, Geo q, float eps,
@@ -522,7 +526,7 @@ __global__ __launch_bounds__(LT) void k_long_in_means(const T* __restrict__ du, 
     }
     long_sums(sq, cr);
     const float inv = inv_rms(sq, inv_n, eps);
-    if (threadIdx.x == 0) means[row] = make_float2(inv, inv * inv * inv * (cr * inv_n));
+    if (threadIdx.x == 0) means[row] = make_float2(inv, inv * (cr * inv_n));
   }
 }
 
@@ -553,10 +557,10 @@ __global__ __launch_bounds__(256) void k_long_in_bwd(
     float g[V], h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float y = rr.get(v), d = rd.get(v);
-      g[v] = fmaf(-mean.y, y, mean.x * (d * rw.get(v)));
+      const float hat = rr.get(v) * mean.x, d = rd.get(v);
+      g[v] = mean.x * fmaf(-mean.y, hat, d * rw.get(v));
       if (dr_out) g[v] += ro.get(v);
-      dw[v] = fmaf(d, y * mean.x, dw[v]);
+      dw[v] = fmaf(d, hat, dw[v]);
       if (s) {
         h[v] = rs.get(v) * g[v];
         ds[v] = fmaf(g[v], rp.get(v), ds[v]);
@@ -642,7 +646,7 @@ __global__ __launch_bounds__(LT) void k_long_out_means(const T* __restrict__ d_o
     }
     long_sums(sq, ct);
     const float inv = inv_rms(sq, inv_n, eps);
-    if (threadIdx.x == 0) means[unit] = make_float2(inv, inv * inv * inv * (ct * inv_n));
+    if (threadIdx.x == 0) means[unit] = make_float2(inv, inv * (ct * inv_n));
   }
 }
 

@@ -418,7 +418,10 @@ ssd_status ssd_prep_amask_backward(const float* A_proj, const float* dt_proj, co
  */
 typedef enum { SSD_INPUT_PLAIN = 0, SSD_INPUT_CONVEX = 1, SSD_INPUT_UNIT = 2 } ssd_input_scale;
 
-/* The largest d_h of the recurrence. */
+/* The largest d_h of the recurrence.  Any number of heads and tokens is taken up to
+ * 2^30 tokens of 64 channels in one head (bf16 forwards 2^31; fewer tokens of more
+ * channels), and 2^34 - 1024 channels in a step; beyond that a launch could not hold
+ * the threads: SSD_ERR_SHAPE. */
 #define SSD_GATED_MAX (1 << 20)
 
 /*
@@ -549,7 +552,7 @@ ssd_status ssd_norm_in_backward(const void* d_out, const float* d_residual_out,
  *   z      [B,N,H d_h] dtype   gate logits Z
  *   weight [H d_h] f32         w
  *   groups                     a divisor of H (1: the whole token, H: each head);
- *                              H d_h / groups <= SSD_NORM_MAX
+ *                              H d_h / groups <= SSD_NORM_MAX, groups <= 2^28 - 32
  *   out    [B,N,H d_h] dtype   out: o
  */
 ssd_status ssd_norm_out(const float* y, const void* z, const float* weight, int64_t B, int64_t H,
@@ -566,7 +569,8 @@ ssd_status ssd_norm_out(const float* y, const void* z, const float* weight, int6
  *   d_out     [B,N,H d_h] dtype  do
  *   dy        [B,H,N,d_h] f32    out (as ssd_backward and ssd_gated_scan_backward take it)
  *   dz        [B,N,H d_h] f32    out
- *   d_weight  [H d_h] f32        out: the sum over b, n (zero when B N = 0)
+ *   d_weight  [H d_h] f32        out: the sum over b, n (zero when B N = 0);
+ *                                H d_h <= 2^27 - 32
  *   workspace                    >= ssd_norm_out_backward_workspace_size bytes
  */
 size_t ssd_norm_out_backward_workspace_size(int64_t B, int64_t H, int64_t N, int64_t d_h,

@@ -712,7 +712,7 @@ static ssd_status gated_sizes(const char* fn, int64_t B, int64_t H, int64_t N, i
     return fail(SSD_ERR_SHAPE, "%s: sizes must be >= 0, d_h >= 1, and their product must not overflow", fn);
   if (d_h > SSD_GATED_MAX)
     return fail(SSD_ERR_UNSUPPORTED, "%s: d_h %lld (at most %d)", fn, (long long)d_h, SSD_GATED_MAX);
-  int64_t wide, slabs;  // a grid holds a workgroup per head, 16 channels and 64 tokens at most
+  int64_t wide, slabs;  // workgroups, were there one to a head, 16 channels and 64 tokens: less than 2^31
   if (!mul_ok(*BH, (d_h + 15) / 16, &slabs) || !mul_ok(slabs, (N + 63) / 64 + 1, &wide) ||
       wide > (int64_t)0x7fffffff)
     return fail(SSD_ERR_SHAPE, "%s: grid too large", fn);
@@ -759,6 +759,7 @@ ssd_status ssd_gated_scan(const void* x, const void* A_proj, const void* I_proj,
       return hip_status(ssd::launch_copy_or_zero(final_state, initial_state, BH * d_h, stream),
                         "final-state copy launch");
     }
+    if (!ssd::gated_scan_fits(dtype == SSD_BF16, BH, N, d_h)) return fail(SSD_ERR_SHAPE, "%s: grid too large", fn);
     if (!x || !A_proj || !y) return fail(SSD_ERR_NULL, "%s: a required pointer is NULL", fn);
     const size_t need = ssd::gated_scan_floats(BH, N, d_h) * sizeof(float);
     if ((s = check_workspace(fn, workspace, workspace_bytes, need)) != SSD_OK) return s;
@@ -786,6 +787,8 @@ ssd_status ssd_gated_scan_step(const void* x, const void* A_proj, const void* I_
     ssd_status s = gated_sizes(fn, S, H, 1, d_h, &SH, &n);
     if (s != SSD_OK || (s = gated_kinds(fn, input_scale, dtype)) != SSD_OK) return s;
     if (n == 0) return SSD_OK;  // no sequences or heads: nothing to compute
+    if ((n + 1023) / 1024 >= (int64_t)1 << 24)  // 256 threads to 1024 channels, and less than 2^32 threads
+      return fail(SSD_ERR_SHAPE, "%s: grid too large", fn);
     if (!x || !A_proj || !state || !new_state) return fail(SSD_ERR_NULL, "%s: a required pointer is NULL", fn);
     const size_t bytes = (size_t)n * (dtype == SSD_BF16 ? 2 : 4);
     const Range ins[] = {{"x", x, bytes}, {"A_proj", A_proj, bytes}, {"I_proj", I_proj, bytes},
@@ -831,6 +834,7 @@ ssd_status ssd_gated_scan_backward(const void* x, const void* A_proj, const void
       return hip_status(ssd::launch_copy_or_zero(d_initial_state, d_final_state, BH * d_h, stream),
                         "initial-state gradient copy launch");
     }
+    if (!ssd::gated_scan_backward_fits(BH, N, d_h)) return fail(SSD_ERR_SHAPE, "%s: grid too large", fn);
     if (!x || !A_proj || !y || !dy || !dx || !dA_proj)
       return fail(SSD_ERR_NULL, "%s: a required pointer is NULL", fn);
     if ((I_proj == nullptr) != (dI_proj == nullptr))
@@ -957,6 +961,9 @@ static ssd_status norm_out_sizes(const char* fn, int64_t B, int64_t H, int64_t N
     return fail(SSD_ERR_SHAPE, "%s: B, N must be >= 0 and the product of the sizes must not overflow", fn);
   if (BN > (int64_t)0x7fffffff || *E > (int64_t)0x7fffffff)
     return fail(SSD_ERR_SHAPE, "%s: more than 2^31 - 1 tokens or channels", fn);
+  // a launch has less than 2^32 threads: up to 32 groups share a workgroup of 512 (fewer where groups are
+  // of more channels, of which 2^31 hold fewer groups)
+  if (groups > ((int64_t)1 << 28) - 32) return fail(SSD_ERR_SHAPE, "%s: grid too large", fn);
   return SSD_OK;
 }
 
@@ -1008,6 +1015,8 @@ ssd_status ssd_norm_out_backward(const void* d_out, const float* y, const void* 
     if (s != SSD_OK || (s = norm_kinds(fn, E / groups, eps, dtype)) != SSD_OK) return s;
     if (gate_first != 0 && gate_first != 1)
       return fail(SSD_ERR_UNSUPPORTED, "%s: gate_first %d (0 or 1)", fn, gate_first);
+    if (E > ((int64_t)1 << 27) - 32)  // the weight gradients' sum has 32 threads a channel
+      return fail(SSD_ERR_SHAPE, "%s: grid too large", fn);
     if (!weight || !d_weight || (n && (!d_out || !y || !z || !dy || !dz)))
       return fail(SSD_ERR_NULL, "%s: a required pointer is NULL", fn);
     const size_t need = n ? ssd::norm_out_backward_floats(B, H, N, d_h, groups) * sizeof(float) : 0;

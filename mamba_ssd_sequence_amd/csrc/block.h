@@ -11,6 +11,7 @@ namespace ssd {
 // The recurrence h_t = a_t h_{t-1} + beta_t g_t x_t over BH independent
 // [N, DH] matrices; scale: ssd_input_scale; I, h0, hf may be NULL.
 size_t gated_scan_floats(int64_t BH, int64_t N, int64_t DH);
+bool gated_scan_fits(bool bf16, int64_t BH, int64_t N, int64_t DH);  // a head fits a launch
 hipError_t launch_gated_scan(bool bf16, int scale, const void* x, const void* A, const void* I,
                              const float* h0, int64_t BH, int64_t N, int64_t DH, float* y,
                              float* hf, float* ws, hipStream_t stream);
@@ -22,6 +23,7 @@ hipError_t launch_gated_scan_step(bool bf16, int scale, const void* x, const voi
 
 // Its gradients; I, dI, h0, dlast, dh0 may be NULL.
 size_t gated_scan_backward_floats(int64_t BH, int64_t N, int64_t DH);
+bool gated_scan_backward_fits(int64_t BH, int64_t N, int64_t DH);
 hipError_t launch_gated_scan_backward(bool bf16, int scale, const void* x, const void* A,
                                       const void* I, const float* h0, const float* y,
                                       const float* dy, const float* dlast, int64_t BH, int64_t N,

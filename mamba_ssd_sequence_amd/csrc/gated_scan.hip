@@ -562,6 +562,46 @@ size_t gated_scan_backward_floats(int64_t BH, int64_t N, int64_t DH) {
   return split_of(BH, N, DH, BWD_TOKENS).floats();
 }
 
+// A launch holds less than 2^32 threads: so many heads go into one (0: a single
+// head has more), and the heads of a call into one launch after the other.
+static int64_t heads_of_launch(const Split& s) {
+  return (int64_t)(0xffffffffu / (unsigned)(s.waves * WAVE)) / s.tiles / s.slabs;
+}
+
+bool gated_scan_fits(bool bf16, int64_t BH, int64_t N, int64_t DH) {
+  return heads_of_launch(split_of(BH, N, DH, fwd_tokens(bf16))) > 0;
+}
+
+bool gated_scan_backward_fits(int64_t BH, int64_t N, int64_t DH) {
+  return heads_of_launch(split_of(BH, N, DH, BWD_TOKENS)) > 0;
+}
+
+// One launch's heads: their number, and where their arrays begin.
+struct Share {
+  int64_t heads, token, state;  // elements of [BH,N,DH] and of [BH,DH] before them
+  unsigned* counters;
+  word_t* words;
+  unsigned grid(const Split& s) const { return (unsigned)(heads * s.tiles); }
+  template <typename T> T* tokens(T* p) const { return p ? p + token : nullptr; }
+  template <typename T> T* states(T* p) const { return p ? p + state : nullptr; }
+};
+
+// calls go(share) for one launch after the other
+template <typename F>
+static hipError_t by_share(const Split& s, int64_t BH, int64_t N, int64_t DH, float* ws, F&& go) {
+  const int64_t most = heads_of_launch(s);
+  for (int64_t b = 0; b < BH; b += most) {
+    Share sh{(BH - b < most ? BH - b : most) * s.slabs, b * N * DH, b * DH, nullptr, nullptr};
+    if (s.tiles > 1) {
+      sh.counters = (unsigned*)ws + b * s.slabs;
+      sh.words = (word_t*)(ws + s.counters()) + b * s.slabs * slab_words(s.tiles, s.C);
+    }
+    const hipError_t e = go(sh);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 // Inputs and outputs pass through once: nontemporal accesses where rows are whole
 // 128-byte lines of fp32 (plain / nontemporal, bf16 with gate: 4 x 16 heads of 2048
 // tokens 19.3 / 18.4 us, 1 x 16 of 65536 144.5 / 129.8; backwards 58.0 / 45.3); else
@@ -605,11 +645,13 @@ hipError_t launch_gated_scan(bool bf16, int scale, const void* x, const void* A,
   return by_call(bf16, scale, I != nullptr, DH, s.waves, [&](auto t, auto sc, auto g, auto k, auto nw) {
     using T = decltype(t);
     using TL = Tile<kind_v(k.value), kind_lpr(k.value), nw.value, fwd_tokens(sizeof(T) == 2)>;
-    hipLaunchKernelGGL((k_gated_scan<T, sc.value, g.value, TL>), dim3((unsigned)(s.heads * s.tiles)),
-                       dim3(TL::NW * WAVE), 0, stream, (const T*)x, (const T*)A, (const T*)I, h0, N,
-                       (int)DH, s.width, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs, passing(DH), y,
-                       hf, (unsigned*)ws, (word_t*)(ws + s.counters()));
-    return hipGetLastError();
+    return by_share(s, BH, N, DH, ws, [&](const Share& sh) {
+      hipLaunchKernelGGL((k_gated_scan<T, sc.value, g.value, TL>), dim3(sh.grid(s)), dim3(TL::NW * WAVE), 0, stream,
+                         sh.tokens((const T*)x), sh.tokens((const T*)A), sh.tokens((const T*)I), sh.states(h0), N,
+                         (int)DH, s.width, (int)s.slabs, (int)sh.heads, (int)s.tiles, s.runs, passing(DH),
+                         sh.tokens(y), sh.states(hf), sh.counters, sh.words);
+      return hipGetLastError();
+    });
   });
 }
 
@@ -635,11 +677,14 @@ hipError_t launch_gated_scan_backward(bool bf16, int scale, const void* x, const
   return by_call(bf16, scale, I != nullptr, DH, s.waves, [&](auto t, auto sc, auto g, auto k, auto nw) {
     using T = decltype(t);
     using TL = Tile<kind_v(k.value), kind_lpr(k.value), nw.value, BWD_TOKENS>;
-    hipLaunchKernelGGL((k_gated_scan_bwd<T, sc.value, g.value, TL>), dim3((unsigned)(s.heads * s.tiles)),
-                       dim3(TL::NW * WAVE), 0, stream, (const T*)x, (const T*)A, (const T*)I, h0, y, dy,
-                       dlast, N, (int)DH, s.width, (int)s.slabs, (int)s.heads, (int)s.tiles, s.runs,
-                       passing(DH), dx, dA, dI, dh0, (unsigned*)ws, (word_t*)(ws + s.counters()));
-    return hipGetLastError();
+    return by_share(s, BH, N, DH, ws, [&](const Share& sh) {
+      hipLaunchKernelGGL((k_gated_scan_bwd<T, sc.value, g.value, TL>), dim3(sh.grid(s)), dim3(TL::NW * WAVE), 0,
+                         stream, sh.tokens((const T*)x), sh.tokens((const T*)A), sh.tokens((const T*)I),
+                         sh.states(h0), sh.tokens(y), sh.tokens(dy), sh.states(dlast), N, (int)DH, s.width,
+                         (int)s.slabs, (int)sh.heads, (int)s.tiles, s.runs, passing(DH), sh.tokens(dx),
+                         sh.tokens(dA), sh.tokens(dI), sh.states(dh0), sh.counters, sh.words);
+      return hipGetLastError();
+    });
   });
 }
 

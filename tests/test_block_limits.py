@@ -1,0 +1,87 @@
+"""Calls at the ends of their sizes: what a launch cannot hold is refused before
+any HIP call or taken in several launches."""
+import pytest
+
+from mamba_ssd_sequence_amd import ssd as binding
+from oracle import block_oracle as K
+
+FAR = [i << 45 for i in range(1, 20)]  # fake addresses 32 TB apart
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return binding.lib()
+
+
+def scan(lib, B, H, N, d, dtype, wsb=0):
+    return lib.ssd_gated_scan(FAR[0], FAR[1], FAR[2], None, B, H, N, d, 2, dtype, FAR[3], None, FAR[4], wsb, None)
+
+
+def scan_back(lib, B, H, N, d, dtype, wsb=0):
+    return lib.ssd_gated_scan_backward(FAR[0], FAR[1], None, None, FAR[3], FAR[4], None, B, H, N, d, 2, dtype, FAR[5],
+                                       FAR[6], None, None, FAR[7], wsb, None)
+
+
+# One head's threads: a tile of 8 waves has 128 tokens of 64 channels (256 in bf16
+# forwards), so 2^23 tiles of 512 threads are 2^32, one more than a launch holds.
+# Without a workspace the largest call that fits is refused for that (6) instead.
+@pytest.mark.parametrize("call,dtype,N,d", [(scan, 0, 1 << 30, 64), (scan, 1, 1 << 31, 64), (scan_back, 1, 1 << 30, 64),
+                                            (scan, 0, 1 << 28, 256), (scan_back, 0, 1 << 28, 200)])
+def test_a_head_larger_than_a_launch(lib, call, dtype, N, d):
+    assert call(lib, 1, 1, N, d, dtype) == 2
+    assert "grid" in lib.ssd_last_error().decode()
+    assert call(lib, 1, 1, N - 256, d, dtype) == 6
+
+
+def test_steps_larger_than_a_launch(lib):
+    step = lambda S, d, out: lib.ssd_gated_scan_step(FAR[0], FAR[1], None, FAR[2], S, 1, d, 0, 1, out, None)  # noqa: E731
+    assert step((1 << 30) - 1, 16, FAR[3]) == 2  # 2^34 - 16 channels: 2^24 workgroups of 256 threads
+    assert step((1 << 30) - 64, 16, None) == 1   # 2^34 - 1024: taken, but for the missing output
+
+
+def test_norm_out_larger_than_a_launch(lib):
+    def fwd(H, d, o):
+        return lib.ssd_norm_out(FAR[0], FAR[1], FAR[2], 1, H, 1, d, H, 1, 1e-5, 1, o, None)
+
+    def back(H, d, dw):
+        return lib.ssd_norm_out_backward(FAR[0], FAR[1], FAR[2], FAR[3], 1, H, 1, d, H, 1, 1e-5, 1, FAR[4], FAR[5], dw,
+                                         FAR[6], 0, None)
+
+    assert fwd(1 << 28, 1, FAR[3]) == 2 and fwd((1 << 28) - 32, 1, None) == 1
+    assert back(1 << 21, 64, FAR[7]) == 2 and back((1 << 21) - 1, 64, None) == 1
+
+
+@pytest.mark.gpu
+def test_more_heads_than_a_launch_holds():
+    """2^23 + 3 heads of 512 threads each: two launches, every copy of the first heads with their bits."""
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    BH, few, N, d = (1 << 23) + 3, 509, 3, 4
+    g = torch.Generator(device="cuda").manual_seed(6)
+
+    def heads(*rest):
+        one = torch.randn((few,) + rest, generator=g, device="cuda")
+        return one.repeat(-(-BH // few), *[1] * len(rest))[:BH].unsqueeze(0).contiguous()
+
+    x, A, I = (heads(N, d).bfloat16() for _ in range(3))
+    dy, h0, dl = heads(N, d), heads(d), heads(d)
+    last = torch.empty_like(h0)
+    y = binding.gated_scan(x, A, I, scale=2, initial_state=h0, final_state=last)
+    grads = binding.gated_scan_backward(x, A, I, y, dy, scale=2, initial_state=h0, d_final_state=dl)
+    torch.cuda.synchronize()
+    assert torch.equal(last, y[:, :, -1])
+    f64 = lambda t: t[:, :few].double().cpu().numpy()  # noqa: E731
+    args = [f64(t) for t in (x, A, I, h0)]
+    back = args + [f64(t) for t in (y, dy, dl)] + [2]
+    for name, got, want, bound in zip(("y", "dx", "dA", "dI", "dh0"), (y, *grads),
+                                      (K.scan(*args, 2), *K.scan_backward(*back)),
+                                      (K.scan_bound(*args, 2), *K.scan_backward_bound(*back))):
+        print("heads past a launch", name, flush=True)
+        assert (abs(f64(got) - want) <= bound).all(), name
+        for a in range(0, BH, few):  # torch's comparisons of whole copies, on the GPU
+            b = min(a + few, BH)
+            if a % (1 << 12) < few or b > BH - 4 * few:
+                assert torch.equal(got[:, a:b], got[:, :b - a]), (name, a)
+        whole = got[0, :BH // few * few].view(BH // few, few, -1)
+        assert bool((whole == whole[:1]).all()), name

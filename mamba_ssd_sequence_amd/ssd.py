@@ -616,7 +616,8 @@ def gated_scan_backward(x, A_proj, I_proj, y, dy, *, scale: int, initial_state=N
 def norm_in(residual, branch, branch_scale, weight, eps: float, *, dtype=None, residual_out=None, out=None):
     """ssd_norm_in: r' = residual + branch_scale branch, u = weight r' / sqrt(mean r'^2 + eps) over the last
     dimension.  residual [..,E] fp32; branch [..,E] bf16 or fp32, or None (then r' is residual, and dtype
-    is u's type); branch_scale [E] fp32 or None (1).  Returns (r' fp32, u of branch's type)."""
+    is u's type); branch_scale [E] fp32 or None (1).  Returns (r' fp32, u of branch's type, which dtype,
+    if given, has to be)."""
     torch = _torch()
     f32 = torch.float32
     i = _first(residual, "residual")[1]
@@ -624,6 +625,8 @@ def norm_in(residual, branch, branch_scale, weight, eps: float, *, dtype=None, r
     E = shape[-1]
     at = _at(residual, "residual", f32, shape, i)
     if branch is not None:
+        if dtype is not None and dtype is not branch.dtype:
+            raise ValueError(f"dtype {dtype} with a branch of {branch.dtype}: the result has the branch's type")
         dtype = branch.dtype
         if residual_out is None:
             residual_out = torch.empty_like(residual)

@@ -85,3 +85,18 @@ def test_more_heads_than_a_launch_holds():
                 assert torch.equal(got[:, a:b], got[:, :b - a]), (name, a)
         whole = got[0, :BH // few * few].view(BH // few, few, -1)
         assert bool((whole == whole[:1]).all()), name
+
+
+@pytest.mark.gpu
+def test_norm_in_refuses_another_type_than_the_branch():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    r, w = torch.randn((3, 64), device="cuda"), torch.ones(64, device="cuda")
+    p = torch.randn_like(r).bfloat16()
+    want = binding.norm_in(r, p, None, w, 1e-5)[1]
+    assert want.dtype == torch.bfloat16
+    assert torch.equal(binding.norm_in(r, p, None, w, 1e-5, dtype=torch.bfloat16)[1], want)
+    for branch, other in ((p, torch.float32), (r, torch.bfloat16), (p, torch.float16)):
+        with pytest.raises(ValueError, match="branch"):
+            binding.norm_in(r, branch, None, w, 1e-5, dtype=other)

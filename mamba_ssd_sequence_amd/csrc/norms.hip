@@ -699,12 +699,18 @@ static bool is_long(int64_t heads, int64_t width) {
 
 // calls f(R) with the row shape for `heads` heads of `width` channels: 8 channels
 // a thread (4 in rows of up to 256), so that a row with its weights and their
-// gradients leaves room for 16 waves a CU and more.  DEEP: 16 channels a thread, a
-// wave to a row of 1024, for norm out forwards, which holds least and whose rows
-// come from many places (2 x 16 heads of 8192 tokens: 23.0 us against 26.9, of 4096
-// 12.1 against 12.8; 1 x 16 of 65536 96 against 92; norm in 8192 rows 16.8 against 16.0).
+// gradients leaves room for 16 waves a CU and more.
+// DEEP, norm out forwards, which holds least and whose rows come from many places:
+// a row of 513 to 1024 channels to one wave, 16 channels a thread and no barrier
+// in its sum, from 2048 rows on, whose workgroups of 8 rows are then one to a CU.
+// One wave / two a row, 16 heads of 64: 256 rows 4.1 / 3.4 us, 1024 4.3 / 3.7, 2048
+// 4.6 / 5.0, 8192 11.9 / 14.7, 2 x 8192 23.0 / 26.9, 32768 48.2 / 50.2, 65536 96.5 /
+// 92.6; 12 heads, 16384 rows 18.8 / 20.9; 8 of 128, 32768 rows 53.1 / 50.4.  Longer rows
+// have their barrier either way, and win with 16 channels as often as they lose
+// (32 heads 0.88 to 1.09 of the time of 8, 64 heads 0.90 to 1.31, 128 heads 0.97 to
+// 1.05); norm in 8192 rows 16.8 / 16.0.  They keep 8.
 template <bool DEEP, typename F>
-static auto by_row(int64_t heads, int64_t width, F&& f) {
+static auto by_row(int64_t heads, int64_t width, int64_t rows, F&& f) {
   const int64_t n = row_pieces(heads, width);
   if (width < 4) {
     if (n <= 64) return f(Row<1, 16, 4>{});
@@ -714,12 +720,8 @@ static auto by_row(int64_t heads, int64_t width, F&& f) {
   if (n <= 32) return f(Row<4, 32, 1>{});
   if (n <= 64) return f(Row<4, 64, 1>{});
   if (n <= 128) return f(Row<4, 64, 2>{});
-  if constexpr (DEEP) {
-    if (n <= 256) return f(Row<4, 64, 4>{});
-    if (n <= 512) return f(Row<4, 128, 4>{});
-    if (n <= 1024) return f(Row<4, 256, 4>{});
-    return f(Row<4, 512, 4>{});
-  }
+  if constexpr (DEEP)
+    if (n <= 256 && rows >= 2048) return f(Row<4, 64, 4>{});
   if (n <= 256) return f(Row<4, 128, 2>{});
   if (n <= 512) return f(Row<4, 256, 2>{});
   if (n <= 1024) return f(Row<4, 512, 2>{});
@@ -757,7 +759,7 @@ static Geo geo_of(R, int64_t tokens, int64_t groups, int64_t heads, int64_t widt
 
 static Geo geo_by(int64_t tokens, int64_t groups, int64_t heads, int64_t width, bool backward,
                   int64_t bytes) {
-  return by_row<false>(heads, width,
+  return by_row<false>(heads, width, tokens * groups,
                        [&](auto row) { return geo_of(row, tokens, groups, heads, width, backward, bytes); });
 }
 
@@ -795,8 +797,8 @@ static hipError_t launch_sum_parts(const float* part, int n, int64_t E, float* o
 
 // calls f(T, row)
 template <bool DEEP = false, typename F>
-static hipError_t by_call(bool bf16, int64_t heads, int64_t width, F&& f) {
-  return by_row<DEEP>(heads, width, [&](auto row) { return bf16 ? f(uint16_t{}, row) : f(float{}, row); });
+static hipError_t by_call(bool bf16, int64_t heads, int64_t width, int64_t rows, F&& f) {
+  return by_row<DEEP>(heads, width, rows, [&](auto row) { return bf16 ? f(uint16_t{}, row) : f(float{}, row); });
 }
 
 hipError_t launch_norm_in(bool bf16, const float* r, const void* p, const float* s, const float* w,
@@ -810,7 +812,7 @@ hipError_t launch_norm_in(bool bf16, const float* r, const void* p, const float*
                          long_geo(rows, 1, 1, E), eps, r_out, (T*)u);
       return hipGetLastError();
     });
-  return by_call(bf16, 1, E, [&](auto t, auto row) {
+  return by_call(bf16, 1, E, rows, [&](auto t, auto row) {
     using T = decltype(t);
     using R = decltype(row);
     const Geo q = geo_of(row, rows, 1, 1, E, false, rows * E * (p ? 8 + 2 * size : 4 + size));
@@ -845,7 +847,7 @@ hipError_t launch_norm_in_backward(bool bf16, const void* du, const float* dr_ou
   const int64_t size = bf16 ? 2 : 4;
   const Geo q = geo_by(rows, 1, 1, E, true, rows * E * (8 + size + (dr_out ? 4 : 0) + (s ? 4 + size : 0)));
   if (rows) {
-    const hipError_t e = by_call(bf16, 1, E, [&](auto t, auto row) {
+    const hipError_t e = by_call(bf16, 1, E, rows, [&](auto t, auto row) {
       using T = decltype(t);
       using R = decltype(row);
       auto go = [&](auto scaled, auto added) {
@@ -875,7 +877,7 @@ hipError_t launch_norm_out(bool bf16, bool gate_first, const float* y, const voi
       };
       return gate_first ? go(std::true_type{}) : go(std::false_type{});
     });
-  return by_call<true>(bf16, H / groups, DH, [&](auto t, auto row) {
+  return by_call<true>(bf16, H / groups, DH, B * N * groups, [&](auto t, auto row) {
     using T = decltype(t);
     using R = decltype(row);
     const Geo q = geo_of(row, B * N, groups, H / groups, DH, false, B * N * H * DH * (bf16 ? 8 : 12));
@@ -918,7 +920,7 @@ hipError_t launch_norm_out_backward(bool bf16, bool gate_first, const void* d_ou
   }
   const Geo q = geo_by(tokens, groups, H / groups, DH, true, tokens * H * DH * (bf16 ? 16 : 20));
   if (tokens) {
-    const hipError_t e = by_call(bf16, H / groups, DH, [&](auto t, auto row) {
+    const hipError_t e = by_call(bf16, H / groups, DH, tokens * groups, [&](auto t, auto row) {
       using T = decltype(t);
       using R = decltype(row);
       auto go = [&](auto first) {

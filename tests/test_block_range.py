@@ -4,7 +4,7 @@ gradients are, whatever the powers of the root would be."""
 import pytest
 
 from oracle import block_oracle as K
-from test_block_gpu import (EPS, _gpu, close, dev, f64, norm_in_inputs, norm_out_inputs, say, ssd,  # noqa: F401
+from test_block_gpu import (EPS, Guard, _gpu, close, dev, f64, norm_in_inputs, norm_out_inputs, say, ssd,  # noqa: F401
                             torch_type)
 
 torch = pytest.importorskip("torch")
@@ -63,3 +63,23 @@ def test_norm_out_sizes(ssd, B, H, N, d, groups, dtype, first, sizes, eps):  # n
     for name, v, want, bound in zip(("dy", "dz", "dw"), got, K.norm_out_backward(*args),
                                     K.norm_out_backward_bound(*args)):
         close(v, want, bound, name)
+
+
+# From 2048 rows on a row of 513 to 1024 channels belongs to one wave forwards.
+MANY = [(1, 16, 2100, 64, 1, "bf16"), (2, 16, 1024, 64, 1, "f32"), (1, 32, 1031, 64, 2, "bf16"),
+        (2100, 11, 1, 60, 1, "bf16"), (3, 17, 700, 33, 1, "f32"), (1, 8, 2047, 128, 1, "bf16"),
+        (1, 1, 2050, 1023, 1, "bf16")]
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("B,H,N,d,groups,dtype", MANY)
+def test_norm_out_many_rows(ssd, B, H, N, d, groups, dtype, first):  # noqa: F811
+    y, z, w, _ = norm_out_inputs(B, H, N, d, dtype, 43)
+    say("norm out", B, H, N, d, groups, dtype, first)
+    out = Guard()
+    o = out.empty((B, N, H * d), torch_type(dtype))
+    ssd.norm_out(y, z, w, EPS, groups=groups, gate_first=first, out=o)
+    torch.cuda.synchronize()
+    out.check()
+    args = [f64(v) for v in (y, z, w)] + [groups, first, EPS]
+    close(o, K.norm_out(*args), K.norm_out_bound(*args, dtype), "o")

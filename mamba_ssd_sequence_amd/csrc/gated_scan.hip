@@ -519,14 +519,22 @@ constexpr int fwd_tokens(bool bf16) { return bf16 ? 8 : 4; }
 constexpr int BWD_TOKENS = 4;
 
 // How a call is cut.  A workgroup of 16 waves has the larger tile, so fewer
-// steps to publish and wait for, but a CU holds only one: it pays where its tiles
-// fill the 256 CUs in whole rounds, up to three and a half (4 x 16 heads of 2048
-// tokens, bf16, one round: 18.1 us against 20.6 of 8 waves; backwards, two: 45.8
-// against 48.8).  Else two workgroups of 8 waves take turns at loading and
-// storing (4 x 16 of 2304 tokens, 1.25 rounds: 24.6 us against 27.0; of 8192, four:
-// 64.9 against 66.0).  With 512 heads and slabs or more the chip is then full
-// without cutting sequences: a workgroup runs its head's tiles one after the
-// other and nothing is published (32 x 16 heads of 2000 tokens: 126 us against 130).
+// steps to publish and wait for, but a CU holds only one: it pays within one round
+// of the 256 CUs and where its tiles fill more than three quarters of two, three
+// or four rounds, short of four whole ones (4 x 16 heads of 2048 tokens, bf16, one
+// round: 17.9 us against 20.4 of 8 waves; of 3500, 1.75: 30.8 against 34.1; backwards
+// 2048, two: 45.6 against 49.1).  Else workgroups of 8 waves take turns at loading
+// and storing (4 x 16 of 2304 tokens, 1.25 rounds: 24.6 us against 27.0; of 8192,
+// four: 65.0 against 65.8).
+// From 512 heads and slabs on the chip can be full without cutting sequences: a
+// workgroup then runs its head's tiles one after the other and nothing is published.
+// That pays for up to 8 tiles a head, if the last round of 256 workgroups leaves
+// less than a tenth of the rounds empty (heads of 600 tokens, one after the other /
+// shared out: 512 39.8 / 45.3 us, backwards 104 / 107; 2048 150 / 161, 404 / 407; 736
+// 58.6 / 62.0; but 528 53.7 / 48.0, backwards 130 / 110.  Of 2048 tokens, 8 tiles, 16
+// backwards: 512 119 / 123, 337 / 333; 528 152 / 128, 424 / 344; 832 211 / 197, 585 / 540.
+// Of 8192: 512 474 / 470, 640 643 / 593.  The border's own losses: 1600 of 300 tokens
+// 73.3 / 78.2, 512 of 2304 140 / 146).
 struct Split {
   int64_t slabs, heads, tiles;  // tiles: those that workgroups of one head share out
   int waves, runs, C, width;    // runs: tiles that a workgroup takes one after the other (then tiles = 1);
@@ -547,7 +555,8 @@ static Split split_of(int64_t BH, int64_t N, int64_t DH, int tokens) {
   const int64_t wide = heads * tiles(16), rounds = (wide + 255) / 256;
   if (rounds <= 1 || (wide < 4 * 256 && 4 * wide > 3 * 256 * rounds))
     return {slabs, heads, tiles(16), 16, 1, C, width};
-  if (heads >= 512) return {slabs, heads, 1, 8, (int)tiles(8), C, width};
+  if (heads >= 512 && tiles(8) <= 8 && 10 * heads > 9 * 256 * ((heads + 255) / 256))
+    return {slabs, heads, 1, 8, (int)tiles(8), C, width};
   return {slabs, heads, tiles(8), 8, 1, C, width};
 }
 

@@ -4,6 +4,7 @@ import pytest
 
 from mamba_ssd_sequence_amd import ssd as binding
 from oracle import block_oracle as K
+from test_block_gpu import SCALES, bounded_backward, bounded_scan, close, dev, f64, say, scan_inputs
 
 FAR = [i << 45 for i in range(1, 20)]  # fake addresses 32 TB apart
 
@@ -100,3 +101,32 @@ def test_norm_in_refuses_another_type_than_the_branch():
     for branch, other in ((p, torch.float32), (r, torch.bfloat16), (p, torch.float16)):
         with pytest.raises(ValueError, match="branch"):
             binding.norm_in(r, branch, None, w, 1e-5, dtype=other)
+
+
+# From 512 heads (and slabs of 64 channels) on, where they fill the chip's rounds, a
+# workgroup takes up to 8 tiles of a head one after the other; else the tiles are
+# shared out (833 heads).  600 tokens are 3 tiles of 64 channels, backwards 5.
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H,N,d,dtype,gate,init,packed", [
+    (64, 8, 600, 64, "bf16", True, True, True), (16, 16, 1000, 80, "bf16", True, False, False),
+    (48, 16, 300, 17, "f32", False, True, False), (128, 4, 2100, 3, "bf16", True, True, True),
+    (119, 7, 300, 64, "f32", True, True, False)])
+def test_scan_of_many_heads(B, H, N, d, dtype, gate, init, packed):
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    for scale in SCALES:
+        t, h0, g = scan_inputs(B, H, N, d, dtype, gate, init, 14, packed)
+        say("scan of many heads", B, H, N, d, dtype, gate, init, packed, scale)
+        y, last = bounded_scan(binding, t, h0, scale)
+        args = [f64(v) for v in t] + [f64(h0)]
+        want, bound = K.scan(*args, scale), K.scan_bound(*args, scale)
+        close(y, want, bound, "y")
+        assert torch.equal(last, y[:, :, -1])
+        dy, dl = dev(g.standard_normal(y.shape)), dev(g.standard_normal(h0.shape)) if init else None
+        got = bounded_backward(binding, t, h0, y, dy, dl, scale)
+        args += [f64(y), f64(dy), f64(dl), scale]
+        for name, v, want, bound in zip(("dx", "dA", "dI", "dh0"), got, K.scan_backward(*args),
+                                        K.scan_backward_bound(*args)):
+            if v is not None:
+                close(v, want, bound, name)

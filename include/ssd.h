@@ -58,7 +58,8 @@ extern "C" {
 typedef enum {
   SSD_OK = 0,
   SSD_ERR_NULL = 1,        /* a required pointer is NULL */
-  SSD_ERR_SHAPE = 2,       /* a size is < 1, or sizes overflow */
+  SSD_ERR_SHAPE = 2,       /* a size is < 1, sizes overflow, or a launch could not hold
+                              their threads (2^32 and more) */
   SSD_ERR_UNSUPPORTED = 3, /* a parameter combination this build does not implement */
   SSD_ERR_ALIGN = 4,       /* a pointer is not 16-byte aligned */
   SSD_ERR_ALIAS = 5,       /* an output overlaps an input or another output */

@@ -61,6 +61,19 @@ bool mul_ok(int64_t a, int64_t b, int64_t* out) {
   return true;
 }
 
+// A launch holds less than 2^32 threads.  HIP does not refuse a larger one: it
+// starts what is left of the threads beyond a multiple of 2^32, without an error.
+bool fits(int64_t workgroups, int64_t threads) { return workgroups <= (int64_t)0xffffffff / threads; }
+
+// Workgroups of a prep call, of 256 threads: a wave takes a chunk, or as many as its lanes hold at 4 tokens a
+// lane where launch_prep takes them so (N a multiple of 4 and 32-bit sizes).
+int64_t prep_workgroups(int64_t BH, int64_t N, int64_t chunk) {
+  const int64_t total = BH * ((N + chunk - 1) / chunk);
+  const bool by_four = N % 4 == 0 && total < ((int64_t)1 << 31) && BH * N < ((int64_t)1 << 32);
+  const int64_t each = 4 * (by_four ? 64 / (chunk / 4) : 1);
+  return (total + each - 1) / each;
+}
+
 struct Range {
   const char* name;
   const void* p;
@@ -150,7 +163,7 @@ ssd_status ssd_prep(const float* dt_proj, const float* dt_bias, const float* A_l
     if (!dt_proj || !dt_bias || !A_log || !dt || !a_cs || !a_chunk)
       return fail(SSD_ERR_NULL, "ssd_prep: a required pointer is NULL");
     const int64_t nc = (N + chunk - 1) / chunk;
-    if ((BH * nc + 3) / 4 > (int64_t)0x7fffffff) return fail(SSD_ERR_SHAPE, "ssd_prep: grid too large");
+    if (!fits(prep_workgroups(BH, N, chunk), 256)) return fail(SSD_ERR_SHAPE, "ssd_prep: grid too large");
     const Range ins[] = {{"dt_proj", dt_proj, (size_t)BHN * 4},
                          {"dt_bias", dt_bias, (size_t)H * 4},
                          {"A_log", A_log, (size_t)H * 4}};
@@ -183,7 +196,7 @@ ssd_status ssd_prep_amask(const float* A_proj, const float* dt_proj, int64_t B, 
     if ((dt_proj == nullptr) != (dt == nullptr))
       return fail(SSD_ERR_NULL, "ssd_prep_amask: dt_proj and dt must both be given or both be NULL");
     const int64_t nc = (N + chunk - 1) / chunk;
-    if ((BH * nc + 3) / 4 > (int64_t)0x7fffffff)
+    if (!fits(prep_workgroups(BH, N, chunk), 256))
       return fail(SSD_ERR_SHAPE, "ssd_prep_amask: grid too large");
     const Range ins[] = {{"A_proj", A_proj, (size_t)BHN * 4}, {"dt_proj", dt_proj, (size_t)BHN * 4}};
     const Range outs[] = {{"dt", dt, (size_t)BHN * 4},
@@ -271,6 +284,18 @@ ssd_status forward_core(const char* fn, bool noalloc, const void* q, const void*
     if (e == hipSuccess) e = ssd::launch_copy_or_zero(final_norm, initial_norm, BH * D, stream);
     return hip_status(e, "final-state copy launch");
   }
+  // the largest grids, of workgroups of 256: the scan's a head (segments only with few heads); else one a
+  // block, at order 1 also one for 256 values of a state, at order 2 16 a head (8 of 512)
+  const int64_t nb = (N + 63) / 64;
+  int64_t grid = BH * nb;
+  if (order == 1 && dtype == SSD_BF16 && ssd::o1_scan_supported(BH, d_h, N)) {
+    grid = BH;
+  } else {
+    const int64_t heads = BH * (order == 1 ? (d_h * d_h + d_h + 255) / 256 : initial_state ? ssd::O2_INIT_PARTS : 16);
+    if (order == 2) grid = 16 * ((BH * ((nb + 1) / 2) + 7) / 8);  // the output kernel's, >= BH nb
+    if (heads > grid) grid = heads;
+  }
+  if (!fits(grid, 256)) return fail(SSD_ERR_SHAPE, "%s: grid too large", fn);
   if (!q || !k || !v || !a_cs || !y) return fail(SSD_ERR_NULL, "%s: a required pointer is NULL", fn);
   const size_t need = ssd::ws_layout(B, H, N, d_h, order).total_floats * sizeof(float);
   if (noalloc) {
@@ -430,7 +455,8 @@ static ssd_status decode_common(const char* fn, const void* q, const void* k, co
   }
   if (!q || !k || !v || !state || !norm_state || !y)
     return fail(SSD_ERR_NULL, "%s: a required pointer is NULL", fn);
-  if (SH > (int64_t)0x7fffffff) return fail(SSD_ERR_SHAPE, "%s: grid too large", fn);
+  if (!fits(SH, order == 1 ? 256 : layout == SSD_STATE_PACKED ? 512 : 1024))
+    return fail(SSD_ERR_SHAPE, "%s: grid too large", fn);
   const int64_t D = order == 1 ? d_h : (layout == SSD_STATE_PACKED ? d_h * (d_h + 1) / 2 : d_h * d_h);
   int64_t nstate;
   if (!mul_ok(SH, D * d_h, &nstate)) return fail(SSD_ERR_SHAPE, "%s: state too large", fn);
@@ -562,7 +588,7 @@ static ssd_status state_layout(const char* fn, bool to_packed, const float* src_
   if (!src_S || !src_z || !dst_S || !dst_z) return fail(SSD_ERR_NULL, "%s: a required pointer is NULL", fn);
   const int64_t Df = d_h * d_h, Dp = d_h * (d_h + 1) / 2;
   int64_t nf, np_;
-  if (!mul_ok(BH, Df * d_h, &nf) || !mul_ok(BH, Dp * d_h, &np_) || BH * d_h > (int64_t)0x7fffffff)
+  if (!mul_ok(BH, Df * d_h, &nf) || !mul_ok(BH, Dp * d_h, &np_) || !fits(BH * d_h, 256))
     return fail(SSD_ERR_SHAPE, "%s: state too large", fn);
   const int64_t ns = to_packed ? nf : np_, nd = to_packed ? np_ : nf;
   const int64_t zs = (to_packed ? Df : Dp) * BH, zd = (to_packed ? Dp : Df) * BH;
@@ -612,6 +638,10 @@ ssd_status ssd_backward(const void* q, const void* k, const void* v, const float
     ssd_status s = validate_forward_sizes(B, H, N, d_h, order, chunk, dtype, &BH, &BHN, &BHNd);
     if (s != SSD_OK) return s;
     if (BHN == 0) return SSD_OK;  // nothing to differentiate
+    // workgroups of 256: one a block, and for 256 values of a state (order 1) or for each feature (order 2)
+    if (!fits(BH * ((N + 63) / 64), 256) ||
+        !fits(BH * (order == 1 ? (d_h * d_h + d_h + 255) / 256 : d_h), 256))
+      return fail(SSD_ERR_SHAPE, "ssd_backward: grid too large");
     if (!q || !k || !v || !a_cs || !y || !den || !dy || !dq || !dk || !dv || !da)
       return fail(SSD_ERR_NULL, "ssd_backward: a required pointer is NULL");
     if ((dt == nullptr) != (ddt == nullptr))
@@ -644,7 +674,7 @@ static ssd_status prep_bwd_sizes(const char* fn, int64_t B, int64_t H, int64_t N
   int64_t BH;
   if (!mul_ok(B, H, &BH) || !mul_ok(BH, N, BHN))
     return fail(SSD_ERR_SHAPE, "%s: B, H, N must be >= 0 and must not overflow", fn);
-  if (H > (int64_t)0x7fffffff) return fail(SSD_ERR_SHAPE, "%s: H too large", fn);
+  if (!fits(H, 1024)) return fail(SSD_ERR_SHAPE, "%s: H too large", fn);  // a workgroup of 1024 a head
   return SSD_OK;
 }
 
@@ -787,7 +817,7 @@ ssd_status ssd_gated_scan_step(const void* x, const void* A_proj, const void* I_
     ssd_status s = gated_sizes(fn, S, H, 1, d_h, &SH, &n);
     if (s != SSD_OK || (s = gated_kinds(fn, input_scale, dtype)) != SSD_OK) return s;
     if (n == 0) return SSD_OK;  // no sequences or heads: nothing to compute
-    if ((n + 1023) / 1024 >= (int64_t)1 << 24)  // 256 threads to 1024 channels, and less than 2^32 threads
+    if (!fits((n + 1023) / 1024, 256))  // 256 threads to 1024 channels
       return fail(SSD_ERR_SHAPE, "%s: grid too large", fn);
     if (!x || !A_proj || !state || !new_state) return fail(SSD_ERR_NULL, "%s: a required pointer is NULL", fn);
     const size_t bytes = (size_t)n * (dtype == SSD_BF16 ? 2 : 4);

@@ -62,9 +62,9 @@ __device__ __forceinline__ void decay_slope(float A, float& a, float& rest, floa
 // one for the outputs, reads x, A_P and I_P twice.  Memory bounds both directions:
 // 1 x 16 heads of 65536 tokens x 64 channels, bf16 with gate, 671 MB that have to
 // move and 677 MB that the counters see, 129 us (5.2 TB/s; a copy of that size
-// makes 5.1); 4 x 16 heads of 2048 tokens 84 MB in 18.1 us (loading, joining and
+// makes 5.1 to 5.3); 4 x 16 heads of 2048 tokens 84 MB in 17.9 us (loading, joining and
 // storing do not overlap when every tile is resident at once), backwards 218 MB in
-// 46 us.  A tile's 39 instruction slots an element would take half of that.
+// 46 to 51 us, by the card.  A tile's 39 instruction slots an element would take half of that.
 //
 // Waiting.  A workgroup takes the next tile of its head from a counter, so the
 // tiles before its own belong to workgroups that have started; each publishes
@@ -354,7 +354,8 @@ __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan(
 // state c_t = a_t lam_t, c_t = a_t (dy_t + c_{t+1}), c_N = d_final_state and
 // lam_t = dy_t + c_{t+1}; c_0 is the gradient of the initial state.  Only A_P
 // and dy are needed for a tile's step; x, I_P and the states before each token
-// (y one token earlier) are read when the tile's entering c is known.
+// (y one token earlier) are loaded right behind them, to arrive while the tiles
+// are joined, and wait in registers for the tile's entering c.
 template <typename T, int SCALE, bool GATE, typename TL>
 __global__ __launch_bounds__(TL::NW* WAVE, 4) void k_gated_scan_bwd(
     const T* __restrict__ x, const T* __restrict__ A, const T* __restrict__ I,
@@ -613,7 +614,7 @@ static hipError_t by_share(const Split& s, int64_t BH, int64_t N, int64_t DH, fl
 
 // Inputs and outputs pass through once: nontemporal accesses where rows are whole
 // 128-byte lines of fp32 (plain / nontemporal, bf16 with gate: 4 x 16 heads of 2048
-// tokens 19.3 / 18.4 us, 1 x 16 of 65536 144.5 / 129.8; backwards 58.0 / 45.3); else
+// tokens 19.0 / 17.8 us, 1 x 16 of 65536 143 / 129; backwards 57.8 / 45.0); else
 // two rows share a line, which has to stay for the second (33 channels,
 // backwards: 34.7 / 59.0).
 static bool passing(int64_t DH) { return DH % 32 == 0; }

@@ -11,9 +11,9 @@
 // All four are bound by memory: every array is read once and written once, a
 // row (a token's group of channels) lives in registers between its sums and its
 // outputs, and norm out reads y where the mixer left it.  bf16, E 1024: norm in
-// 65536 rows 805 MB in 140 us (5.7 TB/s), backwards 8192 rows 168 MB in 33.5 us with
+// 65536 rows 805 MB in 141 us (5.7 TB/s), backwards 8192 rows 168 MB in 33.9 us with
 // the sum of the weight gradients (4 us); norm out 2 x 16 heads of 4096 tokens 67 MB
-// in 12.1 us, backwards 4 x 16 of 2048 134 MB in 26.9 us.
+// in 12.1 us, backwards 4 x 16 of 2048 134 MB in 27.1 us.
 //
 // A row belongs to TPR threads, each with NV pieces of V channels; a workgroup
 // holds NT / TPR rows at a time and walks over the tokens, so that the weights
@@ -28,9 +28,10 @@
 //
 // Rows of more than 2048 pieces (8192 channels) do not fit that way: backwards a
 // thread would hold 128 values and more, and spilled (16384 channels, 1024 rows:
-// 216 us).  A workgroup then walks along a row twice, forwards; backwards one
-// kernel leaves each row's two means, and another takes blocks of 256 pieces down
-// the rows (90 us, 3.7 TB/s of the bytes that have to move).
+// 216 us).  Backwards one kernel then leaves each row's two means, and another takes
+// blocks of 256 pieces down the rows (91 us, 3.7 TB/s of the bytes that have to move).
+// Forwards, where a row would be fewer registers, a workgroup walks along it twice
+// all the same (norm in 1024 x 16384 51 us, 300 x 32768 40 us: 3.9 and 2.9 TB/s).
 #include "block.h"
 #include "common.h"
 #include "elem.h"

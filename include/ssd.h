@@ -419,10 +419,10 @@ ssd_status ssd_prep_amask_backward(const float* A_proj, const float* dt_proj, co
  */
 typedef enum { SSD_INPUT_PLAIN = 0, SSD_INPUT_CONVEX = 1, SSD_INPUT_UNIT = 2 } ssd_input_scale;
 
-/* The largest d_h of the recurrence.  Any number of heads and tokens is taken up to
- * 2^30 tokens of 64 channels in one head (bf16 forwards 2^31; fewer tokens of more
- * channels), and 2^34 - 1024 channels in a step; beyond that a launch could not hold
- * the threads: SSD_ERR_SHAPE. */
+/* The largest d_h of the recurrence.  SSD_ERR_SHAPE: 2^31 pieces of 16 channels and
+ * 64 tokens (with one more piece of tokens a head) and beyond; a single head of 2^30
+ * tokens of 64 channels (bf16 forwards 2^31; fewer tokens of more channels) and beyond;
+ * steps of more than 2^34 - 1024 channels. */
 #define SSD_GATED_MAX (1 << 20)
 
 /*
